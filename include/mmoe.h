@@ -388,6 +388,61 @@ mmoe_status mmoe_profile_read(mmoe_handle* h, int32_t* launches, double* total_m
 mmoe_status mmoe_forward_static_scratch(const mmoe_config* cfg, const mmoe_weights* w, const uint16_t* x_bf16,
                                         int64_t T, float* y, void* stream);
 
+/* ---- 8-bit floating point (e4m3) with a scale per block of 128 ------------
+ * A quantised block has the scale s = max|v| / 448 and the codes e4m3(v / s)
+ * (IEEE FP32 divisions, round to nearest even); a block of zeros has s = 0 and
+ * codes 0.  A NaN in a block makes s NaN, an infinity makes it infinite, and
+ * products with the block NaN.  An activation row has one block per 128
+ * consecutive features, a weight matrix one per 128 x 128 values; the last
+ * blocks of a row or matrix may be partial.  With KB = ceil(K / 128):
+ *   rows     codes uint8 [rows, K], scales FP32 [rows, KB]
+ *   weights  codes uint8 [N, K],    scales FP32 [ceil(N / 128), KB]
+ *
+ * These calls keep no state: they run on the current device, which must own
+ * every buffer, on any stream, also in a stream capture, and calls on buffers
+ * of their own may overlap on the GPU.  Outputs must not overlap inputs.
+ * Errors of all of them: INVALID_ARG (a NULL pointer, a size, stride, type or
+ * alignment out of range, overlapping buffers), CUDA, and from the products
+ * TIMEOUT (a bounded wait of an earlier call on this device gave up). */
+enum { MMOE_F32 = 0, MMOE_BF16 = 1 }; /* element types of x, w and y below */
+
+/* x [rows, K] (FP32 or BF16, row stride ldx elements) to codes and scales.
+ * K a multiple of 8; x 16-byte aligned, ldx a multiple of 16 bytes; q 8-byte aligned. */
+mmoe_status mmoe_quantize_fp8_rows(const void* x, int32_t x_type, int64_t rows, int64_t K, int64_t ldx, uint8_t* q,
+                                   float* s, void* stream);
+
+/* w [batch, N, K] (FP32 or BF16, contiguous) to codes [batch, N, K] and scales
+ * [batch, ceil(N / 128), KB].  K a multiple of 8; w 16-byte, q 8-byte aligned. */
+mmoe_status mmoe_quantize_fp8_blocks(const void* w, int32_t w_type, int64_t batch, int64_t N, int64_t K, uint8_t* q,
+                                     float* s, void* stream);
+
+/* y[M, N] = a[M, K] w[N, K]^T from codes and scales: per block of K the FP32
+ * sum of the products of codes, times both scales, added in FP32 over the
+ * blocks and rounded once to y's type (row stride ldy elements).  M = 0 is a
+ * no-op.  K a multiple of 16; N any; a and w 16-byte aligned. */
+mmoe_status mmoe_gemm_fp8(const uint8_t* a, const float* sa, int64_t M, const uint8_t* w, const float* sw, int64_t N,
+                          int64_t K, void* y, int32_t y_type, int64_t ldy, void* stream);
+
+/* The same product over rows sorted by group (expert): rows offsets[g] ..
+ * offsets[g + 1] - 1 of a use weight matrix g of w [groups, N, K] (scales
+ * [groups, ceil(N / 128), KB]).  offsets: int32 [groups + 1] on the device;
+ * entries out of [0, M] or out of order are taken as the nearest ones that are
+ * not.  Rows of y before offsets[0] and from offsets[groups] on are left as
+ * they were.  1 <= groups <= 1024. */
+mmoe_status mmoe_gemm_fp8_grouped(const uint8_t* a, const float* sa, int64_t M, const int32_t* offsets, int64_t groups,
+                                  const uint8_t* w, const float* sw, int64_t N, int64_t K, void* y, int32_t y_type,
+                                  int64_t ldy, void* stream);
+
+/* mmoe_quantize_fp8_rows of x (BF16, row stride ldx, a multiple of 8), then
+ * mmoe_gemm_fp8, with the same results.  Up to 64 rows run as one launch that
+ * quantises on the way in; more need a workspace (device, 16-byte aligned) of
+ * the bytes that mmoe_linear_fp8_workspace writes to *bytes (0 for up to 64
+ * rows); it holds nothing between calls. */
+mmoe_status mmoe_linear_fp8_workspace(int64_t M, int64_t K, size_t* bytes);
+mmoe_status mmoe_linear_fp8(const uint16_t* x_bf16, int64_t M, int64_t ldx, const uint8_t* w, const float* sw, int64_t N,
+                            int64_t K, void* y, int32_t y_type, int64_t ldy, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
 #ifdef __cplusplus
 }
 #endif

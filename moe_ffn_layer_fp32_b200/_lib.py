@@ -32,8 +32,12 @@ STAGE_XQ, STAGE_SX, STAGE_OFFSETS, STAGE_ROW_SRC, STAGE_SLOT_ROW, STAGE_HQ, STAG
 EXPORTS = ("mmoe_create", "mmoe_load_quantized_weights", "mmoe_forward", "mmoe_forward_host", "mmoe_destroy",
            "mmoe_last_error", "mmoe_quantize_int4", "mmoe_debug_copy_stage", "mmoe_debug_partials",
            "mmoe_profile_enable", "mmoe_profile_read", "mmoe_forward_static_scratch", "mmoe_debug_host_chunks",
-           "mmoe_debug_set_wait_limit", "mmoe_debug_fail_alloc", "mmoe_forward_chain")
+           "mmoe_debug_set_wait_limit", "mmoe_debug_fail_alloc", "mmoe_forward_chain",
+           "mmoe_quantize_fp8_rows", "mmoe_quantize_fp8_blocks", "mmoe_gemm_fp8", "mmoe_gemm_fp8_grouped",
+           "mmoe_linear_fp8_workspace", "mmoe_linear_fp8")
 MAX_CHAIN_LAYERS = 32
+
+F32, BF16 = 0, 1  # element types of the e4m3 operators and the block norm
 
 STATIC_SCRATCH_BYTES = 8 * 1024 * 1024
 
@@ -88,6 +92,12 @@ def lib() -> C.CDLL:
     L.mmoe_debug_set_wait_limit.argtypes = [vp, i64, i32]
     L.mmoe_debug_fail_alloc.argtypes = [i64]
     L.mmoe_forward_chain.argtypes = [C.POINTER(vp), i32, vp, i64, C.POINTER(vp), vp]
+    L.mmoe_quantize_fp8_rows.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+    L.mmoe_quantize_fp8_blocks.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+    L.mmoe_gemm_fp8.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, i32, i64, vp]
+    L.mmoe_gemm_fp8_grouped.argtypes = [vp, vp, i64, vp, i64, vp, vp, i64, i64, vp, i32, i64, vp]
+    L.mmoe_linear_fp8_workspace.argtypes = [i64, i64, C.POINTER(C.c_size_t)]
+    L.mmoe_linear_fp8.argtypes = [vp, i64, i64, vp, vp, i64, i64, vp, i32, i64, vp, C.c_size_t, vp]
     for name in EXPORTS:
         if name != "mmoe_last_error":
             getattr(L, name).restype = st

@@ -1,0 +1,126 @@
+// Quantisation to e4m3 codes with one FP32 scale per block of 128.
+//
+// Both kernels read every value once, keep it in registers between the
+// maximum and the division, and write one byte a value: they are bound by
+// memory (3 bytes a value for BF16 rows).
+#include "fp8.cuh"
+
+namespace mmoe {
+namespace f8 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kItems = 4;  // blocks a half warp holds at once: enough loads in flight to cover the latency
+
+// Rows: a half warp takes one (row, block) at a time, 8 values a lane (16 bytes of BF16).
+template <class T>
+__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const T* x, int64_t nblk, int kb, int K,
+                                                                 int64_t ldx, uint8_t* q,
+                                                                 float* s)
+{
+    const int hl = threadIdx.x & 15;
+    dep_launch();
+    dep_wait();
+    const int64_t first = ((int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4)) * kItems;
+    float v[kItems][8];
+    int64_t row[kItems];
+    int col[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int64_t b = first + i;
+        row[i] = b / kb;
+        col[i] = (int)(b - row[i] * kb) * kBlk + hl * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+        if (b < nblk && col[i] < K) load8(x + row[i] * ldx + col[i], v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const float sc = scale_of(half_warp_max(amax8(v[i])));
+        if (first + i >= nblk) continue;
+        if (hl == 0) s[first + i] = sc;
+        if (col[i] < K)
+            *reinterpret_cast<uint2*>(q + row[i] * K + col[i]) = make_uint2(e4m3x4(v[i], sc), e4m3x4(v[i] + 4, sc));
+    }
+}
+
+// Weights: one CTA per 128 x 128 block; a half warp takes a row at a time.
+template <class T>
+__global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(const T* w, int nb, int kb, int N,
+                                                                   int K, uint8_t* q,
+                                                                   float* s)
+{
+    constexpr int kRows = kBlk / (kThreads / 16);
+    __shared__ uint32_t part[kThreads / 32];
+    const int hl = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+    const int64_t blk = blockIdx.x;  // (batch * nb + row block) * kb + column block
+    const int64_t bn = blk / kb;
+    const int col = (int)(blk - bn * kb) * kBlk + hl * 8;
+    const int64_t batch = bn / nb;
+    const int n0 = (int)(bn - batch * nb) * kBlk;
+    dep_launch();
+    dep_wait();
+    float v[kRows][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int n = n0 + r0 + i * (kThreads / 16);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+        if (n < N && col < K) load8(w + (batch * N + n) * K + col, v[i]);
+        m = max(m, amax8(v[i]));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) m = max(m, part[i]);
+    const float sc = scale_of(m);
+    if (threadIdx.x == 0) s[blk] = sc;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int n = n0 + r0 + i * (kThreads / 16);
+        if (n < N && col < K)
+            *reinterpret_cast<uint2*>(q + (batch * N + n) * K + col) =
+                make_uint2(e4m3x4(v[i], sc), e4m3x4(v[i] + 4, sc));
+    }
+}
+
+cudaLaunchConfig_t dependent(unsigned grid, cudaStream_t st, cudaLaunchAttribute* at) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    at->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at->val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(const void* x, bool bf16, int64_t rows, int64_t K, int64_t ldx, uint8_t* q, float* s,
+                                 cudaStream_t st) {
+    const int64_t kb = blocks_of(K), nblk = rows * kb, per = kThreads / 16 * kItems;
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t cfg = dependent((unsigned)((nblk + per - 1) / per), st, &at);
+    return bf16 ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<__nv_bfloat16>, (const __nv_bfloat16*)x, nblk, (int)kb,
+                                     (int)K, ldx, q, s)
+                : cudaLaunchKernelEx(&cfg, quantize_rows_kernel<float>, (const float*)x, nblk, (int)kb, (int)K, ldx, q,
+                                     s);
+}
+
+cudaError_t launch_quantize_blocks(const void* w, bool bf16, int64_t batch, int64_t N, int64_t K, uint8_t* q, float* s,
+                                   cudaStream_t st) {
+    const int64_t nb = blocks_of(N), kb = blocks_of(K);
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t cfg = dependent((unsigned)(batch * nb * kb), st, &at);
+    return bf16 ? cudaLaunchKernelEx(&cfg, quantize_blocks_kernel<__nv_bfloat16>, (const __nv_bfloat16*)w, (int)nb,
+                                     (int)kb, (int)N, (int)K, q, s)
+                : cudaLaunchKernelEx(&cfg, quantize_blocks_kernel<float>, (const float*)w, (int)nb, (int)kb, (int)N,
+                                     (int)K, q, s);
+}
+
+}  // namespace f8
+}  // namespace mmoe

@@ -37,6 +37,21 @@ mmoe_status cuda_fail(cudaError_t e, const char* what) {
                 cudaGetErrorString(e), cudaGetErrorName(e));
 }
 
+}  // namespace
+
+mmoe_status mmoe::report(mmoe_status st, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return fail(st, "%s", buf);
+}
+
+mmoe_status mmoe::report_cuda(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+
+namespace {
+
 #define MMOE_CUDA(call, what)                          \
     do {                                               \
         cudaError_t e_ = (call);                       \

@@ -87,6 +87,10 @@ inline int64_t max_tiles_for(int64_t T, int k, int E, int tile_rows = kTileRows)
     return (T * k + tile_rows - 1) / tile_rows + E + (T + tile_rows - 1) / tile_rows + 1;
 }
 
+// Sets the thread's last-error text (mmoe_last_error) and returns `st`; a CUDA error as OOM or CUDA.
+mmoe_status report(mmoe_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+mmoe_status report_cuda(cudaError_t e, const char* what);
+
 // launchers (each returns the launch error, if any)
 cudaError_t launch_router_quant(const Plan& p, cudaStream_t s);
 bool router_mma_supported(int d, int E);

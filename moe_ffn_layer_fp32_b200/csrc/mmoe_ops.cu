@@ -1,0 +1,233 @@
+// C entries of the stateless operators (declared in include/mmoe.h): the e4m3
+// quantisers and products.
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "fp8.cuh"
+#include "mmoe_internal.cuh"
+
+using namespace mmoe;
+
+namespace {
+
+// What the kernels' bounded waits report to: one word of mapped host memory per device, allocated by
+// the device's first call (also inside a stream capture) and kept until the process ends.
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+int* g_flag[kMaxDevices] = {};
+
+mmoe_status device_flag(int** flag) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return report_cuda(e, "cudaGetDevice");
+    if (dev < 0 || dev >= kMaxDevices) return report(MMOE_ERR_INVALID_ARG, "device %d: unsupported index", dev);
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (!g_flag[dev]) {
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        int* p = nullptr;
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        e = cudaHostAlloc(reinterpret_cast<void**>(&p), sizeof(int), cudaHostAllocMapped | cudaHostAllocPortable);
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e != cudaSuccess) return report_cuda(e, "flag allocation");
+        *p = 0;
+        g_flag[dev] = p;  // device and host address are the same under unified addressing
+    }
+    volatile int* v = g_flag[dev];
+    if (*v != 0) {
+        const int site = *v;
+        *v = 0;
+        return report(MMOE_ERR_TIMEOUT, "a kernel of an earlier call gave up waiting (site %d)", site);
+    }
+    *flag = g_flag[dev];
+    return MMOE_OK;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// [a, a + n) and [b, b + m) share a byte
+bool overlap(const void* a, int64_t n, const void* b, int64_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return n > 0 && m > 0 && x < y + (uintptr_t)m && y < x + (uintptr_t)n;
+}
+
+mmoe_status check_type(int32_t t, const char* what) {
+    if (t != MMOE_F32 && t != MMOE_BF16) return report(MMOE_ERR_INVALID_ARG, "%s=%d: must be MMOE_F32 or MMOE_BF16", what, t);
+    return MMOE_OK;
+}
+
+int64_t size_of(int32_t t) { return t == MMOE_BF16 ? 2 : 4; }
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 256;
+constexpr int64_t kMaxDim = 1 << 20;
+
+mmoe_status check_dim(int64_t v, const char* what, int64_t step) {
+    if (v < step || v > kMaxDim || v % step)
+        return report(MMOE_ERR_INVALID_ARG, "%s=%lld: must be a multiple of %lld in [%lld, 2^20]", what, (long long)v,
+                      (long long)step, (long long)step);
+    return MMOE_OK;
+}
+
+mmoe_status check_rows(int64_t v, const char* what) {
+    if (v < 0 || v > kMaxRows) return report(MMOE_ERR_INVALID_ARG, "%s=%lld: must be in [0, 2^31 - 256]", what, (long long)v);
+    return MMOE_OK;
+}
+
+#define CHECK(x)                               \
+    do {                                       \
+        const mmoe_status st_ = (x);           \
+        if (st_ != MMOE_OK) return st_;        \
+    } while (0)
+
+// What the dense, the fused and the grouped product share.
+mmoe_status check_product(int64_t M, const uint8_t* w, const float* sw, int64_t G, int64_t N, int64_t K, const void* y,
+                          int32_t y_type, int64_t ldy) {
+    CHECK(check_rows(M, "M"));
+    CHECK(check_dim(N, "N", 1));
+    CHECK(check_dim(K, "K", 16));
+    CHECK(check_type(y_type, "y_type"));
+    if (ldy < N) return report(MMOE_ERR_INVALID_ARG, "ldy=%lld: must be at least N=%lld", (long long)ldy, (long long)N);
+    if (G * N > kMaxRows || G * f8::blocks_of(N) * f8::blocks_of(K) > kMaxRows)
+        return report(MMOE_ERR_INVALID_ARG, "the weights have too many rows or blocks");
+    if (M == 0) return MMOE_OK;
+    if (!w || !sw || !y) return report(MMOE_ERR_INVALID_ARG, "a pointer is NULL");
+    if (!aligned16(w)) return report(MMOE_ERR_INVALID_ARG, "the weight codes must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(y) % size_of(y_type) || reinterpret_cast<uintptr_t>(sw) % 4)
+        return report(MMOE_ERR_INVALID_ARG, "y and the scales must be aligned to their elements");
+    const int64_t yb = ((M - 1) * ldy + N) * size_of(y_type);
+    if (overlap(y, yb, w, G * N * K) || overlap(y, yb, sw, G * f8::blocks_of(N) * f8::blocks_of(K) * 4))
+        return report(MMOE_ERR_INVALID_ARG, "y overlaps the weights");
+    return MMOE_OK;
+}
+
+mmoe_status check_codes(const uint8_t* a, const float* sa, int64_t M, int64_t K, const void* y, int64_t yb) {
+    if (M == 0) return MMOE_OK;
+    if (!a || !sa) return report(MMOE_ERR_INVALID_ARG, "a pointer is NULL");
+    if (!aligned16(a) || reinterpret_cast<uintptr_t>(sa) % 4)
+        return report(MMOE_ERR_INVALID_ARG, "the codes must be 16-byte aligned, the scales 4-byte aligned");
+    if (overlap(y, yb, a, M * K) || overlap(y, yb, sa, M * f8::blocks_of(K) * 4))
+        return report(MMOE_ERR_INVALID_ARG, "y overlaps the codes or scales of a");
+    return MMOE_OK;
+}
+
+// mmoe_linear_fp8's workspace: the scales, then the codes of x.
+size_t scale_bytes(int64_t M, int64_t K) { return (size_t)(M * f8::blocks_of(K) * 4 + 15) / 16 * 16; }
+size_t linear_workspace(int64_t M, int64_t K) { return M <= f8::kSmallRows ? 0 : scale_bytes(M, K) + (size_t)(M * K); }
+
+}  // namespace
+
+extern "C" {
+
+mmoe_status mmoe_quantize_fp8_rows(const void* x, int32_t x_type, int64_t rows, int64_t K, int64_t ldx, uint8_t* q,
+                                   float* s, void* stream) {
+    CHECK(check_rows(rows, "rows"));
+    CHECK(check_dim(K, "K", 8));
+    CHECK(check_type(x_type, "x_type"));
+    const int64_t es = size_of(x_type), kb = f8::blocks_of(K);
+    if (ldx < K || ldx % (16 / es))
+        return report(MMOE_ERR_INVALID_ARG, "ldx=%lld: must be at least K and whole 16 bytes", (long long)ldx);
+    if (rows == 0) return MMOE_OK;
+    if (rows * kb > (int64_t(1) << 36)) return report(MMOE_ERR_INVALID_ARG, "too many blocks");
+    if (!x || !q || !s) return report(MMOE_ERR_INVALID_ARG, "a pointer is NULL");
+    if (!aligned16(x) || reinterpret_cast<uintptr_t>(q) % 8 || reinterpret_cast<uintptr_t>(s) % 4)
+        return report(MMOE_ERR_INVALID_ARG, "x must be 16-byte, q 8-byte and s 4-byte aligned");
+    const int64_t xb = ((rows - 1) * ldx + K) * es;
+    if (overlap(x, xb, q, rows * K) || overlap(x, xb, s, rows * kb * 4) || overlap(q, rows * K, s, rows * kb * 4))
+        return report(MMOE_ERR_INVALID_ARG, "x, q and s must not overlap");
+    const cudaError_t e = f8::launch_quantize_rows(x, x_type == MMOE_BF16, rows, K, ldx, q, s, (cudaStream_t)stream);
+    return e == cudaSuccess ? MMOE_OK : report_cuda(e, "quantise rows launch");
+}
+
+mmoe_status mmoe_quantize_fp8_blocks(const void* w, int32_t w_type, int64_t batch, int64_t N, int64_t K, uint8_t* q,
+                                     float* s, void* stream) {
+    CHECK(check_rows(batch, "batch"));
+    CHECK(check_dim(N, "N", 1));
+    CHECK(check_dim(K, "K", 8));
+    CHECK(check_type(w_type, "w_type"));
+    if (batch == 0) return MMOE_OK;
+    const int64_t es = size_of(w_type), nblk = batch * f8::blocks_of(N) * f8::blocks_of(K), n = batch * N * K;
+    if (nblk > kMaxRows) return report(MMOE_ERR_INVALID_ARG, "too many blocks");
+    if (!w || !q || !s) return report(MMOE_ERR_INVALID_ARG, "a pointer is NULL");
+    if (!aligned16(w) || reinterpret_cast<uintptr_t>(q) % 8 || reinterpret_cast<uintptr_t>(s) % 4)
+        return report(MMOE_ERR_INVALID_ARG, "w must be 16-byte, q 8-byte and s 4-byte aligned");
+    if (overlap(w, n * es, q, n) || overlap(w, n * es, s, nblk * 4) || overlap(q, n, s, nblk * 4))
+        return report(MMOE_ERR_INVALID_ARG, "w, q and s must not overlap");
+    const cudaError_t e = f8::launch_quantize_blocks(w, w_type == MMOE_BF16, batch, N, K, q, s, (cudaStream_t)stream);
+    return e == cudaSuccess ? MMOE_OK : report_cuda(e, "quantise blocks launch");
+}
+
+mmoe_status mmoe_gemm_fp8(const uint8_t* a, const float* sa, int64_t M, const uint8_t* w, const float* sw, int64_t N,
+                          int64_t K, void* y, int32_t y_type, int64_t ldy, void* stream) {
+    CHECK(check_product(M, w, sw, 1, N, K, y, y_type, ldy));
+    CHECK(check_codes(a, sa, M, K, y, ((M - 1) * ldy + N) * size_of(y_type)));
+    if (M == 0) return MMOE_OK;
+    f8::Product p = {a, sa, nullptr, 0, w, sw, M, (int)N, (int)K, 0, nullptr, y, y_type == MMOE_BF16, ldy, nullptr};
+    CHECK(device_flag(&p.err));
+    const cudaError_t e = M <= f8::kSmallRows ? f8::launch_product_small(p, (cudaStream_t)stream)
+                                              : f8::launch_product(p, (cudaStream_t)stream);
+    return e == cudaSuccess ? MMOE_OK : report_cuda(e, "product launch");
+}
+
+mmoe_status mmoe_gemm_fp8_grouped(const uint8_t* a, const float* sa, int64_t M, const int32_t* offsets, int64_t groups,
+                                  const uint8_t* w, const float* sw, int64_t N, int64_t K, void* y, int32_t y_type,
+                                  int64_t ldy, void* stream) {
+    if (groups < 1 || groups > f8::kMaxGroups)
+        return report(MMOE_ERR_INVALID_ARG, "groups=%lld: must be in [1, %d]", (long long)groups, f8::kMaxGroups);
+    CHECK(check_product(M, w, sw, groups, N, K, y, y_type, ldy));
+    CHECK(check_codes(a, sa, M, K, y, ((M - 1) * ldy + N) * size_of(y_type)));
+    if (M == 0) return MMOE_OK;
+    if (!offsets || reinterpret_cast<uintptr_t>(offsets) % 4)
+        return report(MMOE_ERR_INVALID_ARG, "offsets is NULL or misaligned");
+    if (overlap(y, ((M - 1) * ldy + N) * size_of(y_type), offsets, 4 * (groups + 1)))
+        return report(MMOE_ERR_INVALID_ARG, "y overlaps the offsets");
+    f8::Product p = {a, sa, nullptr, 0, w, sw, M, (int)N, (int)K, (int)groups, offsets, y, y_type == MMOE_BF16, ldy,
+                     nullptr};
+    CHECK(device_flag(&p.err));
+    const cudaError_t e = f8::launch_product(p, (cudaStream_t)stream);
+    return e == cudaSuccess ? MMOE_OK : report_cuda(e, "grouped product launch");
+}
+
+mmoe_status mmoe_linear_fp8_workspace(int64_t M, int64_t K, size_t* bytes) {
+    if (!bytes) return report(MMOE_ERR_INVALID_ARG, "bytes is NULL");
+    CHECK(check_rows(M, "M"));
+    CHECK(check_dim(K, "K", 16));
+    *bytes = linear_workspace(M, K);
+    return MMOE_OK;
+}
+
+mmoe_status mmoe_linear_fp8(const uint16_t* x_bf16, int64_t M, int64_t ldx, const uint8_t* w, const float* sw, int64_t N,
+                            int64_t K, void* y, int32_t y_type, int64_t ldy, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+    CHECK(check_product(M, w, sw, 1, N, K, y, y_type, ldy));
+    if (ldx < K || ldx % 8)
+        return report(MMOE_ERR_INVALID_ARG, "ldx=%lld: must be at least K and a multiple of 8", (long long)ldx);
+    if (M == 0) return MMOE_OK;
+    if (!x_bf16 || !aligned16(x_bf16)) return report(MMOE_ERR_INVALID_ARG, "x is NULL or not 16-byte aligned");
+    const int64_t xb = ((M - 1) * ldx + K) * 2, yb = ((M - 1) * ldy + N) * size_of(y_type);
+    if (overlap(x_bf16, xb, y, yb)) return report(MMOE_ERR_INVALID_ARG, "x and y overlap");
+    f8::Product p = {nullptr, nullptr, reinterpret_cast<const __nv_bfloat16*>(x_bf16), ldx, w, sw, M, (int)N, (int)K, 0,
+                     nullptr, y, y_type == MMOE_BF16, ldy, nullptr};
+    const cudaStream_t st = (cudaStream_t)stream;
+    if (M <= f8::kSmallRows) {
+        CHECK(device_flag(&p.err));
+        const cudaError_t e = f8::launch_product_small(p, st);
+        return e == cudaSuccess ? MMOE_OK : report_cuda(e, "linear launch");
+    }
+    const size_t need = linear_workspace(M, K);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need)
+        return report(MMOE_ERR_INVALID_ARG, "the workspace must be 16-byte aligned and %zu bytes long", need);
+    if (overlap(workspace, (int64_t)need, y, yb) || overlap(workspace, (int64_t)need, x_bf16, xb) ||
+        overlap(workspace, (int64_t)need, w, N * K))
+        return report(MMOE_ERR_INVALID_ARG, "the workspace overlaps x, y or the weights");
+    CHECK(device_flag(&p.err));
+    float* s = static_cast<float*>(workspace);
+    uint8_t* q = static_cast<uint8_t*>(workspace) + scale_bytes(M, K);
+    cudaError_t e = f8::launch_quantize_rows(x_bf16, true, M, K, ldx, q, s, st);
+    p.a = q;
+    p.sa = s;
+    p.x = nullptr;
+    if (e == cudaSuccess) e = f8::launch_product(p, st);
+    return e == cudaSuccess ? MMOE_OK : report_cuda(e, "linear launch");
+}
+
+}  // extern "C"
