@@ -443,6 +443,45 @@ mmoe_status mmoe_linear_fp8(const uint16_t* x_bf16, int64_t M, int64_t ldx, cons
                             int64_t K, void* y, int32_t y_type, int64_t ldy, void* workspace, size_t workspace_bytes,
                             void* stream);
 
+/* ---- between two blocks -----------------------------------------------------
+ * The norm after a block, the block's gate, the residual update and the norm
+ * before the next block, for every row:
+ *
+ *   z  = y rsqrt(mean(y^2) + eps) w_post        (z = y where w_post is NULL)
+ *   r' = residual_scale r + gate z              (gate 1 where NULL; residual_scale r where y is NULL)
+ *   x  = r' rsqrt(mean(r'^2) + eps) w_pre       (not computed where w_pre is NULL)
+ *
+ * in FP32; r' is rounded to r's type where it is stored, x is computed from
+ * the sum before that rounding, and the codes xq, sx (e4m3, as above) from x
+ * before its rounding to BF16.  Infinities and NaN stay within their row.
+ * r_out may be r itself (same address and stride); no other output may overlap
+ * an input or another output.  Runs on the current device; keeps no state.
+ * Errors: INVALID_ARG, CUDA. */
+typedef struct {
+    int64_t rows;          /* 0: no-op */
+    int32_t d;             /* features, a multiple of 8 in [8, 8192] */
+    int32_t r_type;        /* MMOE_F32 or MMOE_BF16: r and r_out */
+    int32_t y_type;        /* of y */
+    int32_t gate_col;      /* 1: a gate for each feature, 0: one for the row */
+    int64_t gate_row;      /* elements between the gates of two rows (0: the same for all) */
+    float residual_scale;
+    float eps;
+    const void* r;         /* [rows, d], row stride ldr elements; strided tensors are 16-byte aligned, rows too */
+    int64_t ldr;
+    const void* y;         /* [rows, d], row stride ldy, or NULL */
+    int64_t ldy;
+    const float* w_post;   /* [d] or NULL */
+    const float* gate;     /* or NULL */
+    const float* w_pre;    /* [d] or NULL */
+    void* r_out;           /* [rows, d], row stride ldo, or NULL */
+    int64_t ldo;
+    uint16_t* x;           /* BF16 [rows, d] or NULL */
+    uint8_t* xq;           /* codes [rows, d] or NULL */
+    float* sx;             /* scales [rows, ceil(d / 128)], with xq */
+} mmoe_norm;
+
+mmoe_status mmoe_block_norm(const mmoe_norm* n, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -34,7 +34,7 @@ EXPORTS = ("mmoe_create", "mmoe_load_quantized_weights", "mmoe_forward", "mmoe_f
            "mmoe_profile_enable", "mmoe_profile_read", "mmoe_forward_static_scratch", "mmoe_debug_host_chunks",
            "mmoe_debug_set_wait_limit", "mmoe_debug_fail_alloc", "mmoe_forward_chain",
            "mmoe_quantize_fp8_rows", "mmoe_quantize_fp8_blocks", "mmoe_gemm_fp8", "mmoe_gemm_fp8_grouped",
-           "mmoe_linear_fp8_workspace", "mmoe_linear_fp8")
+           "mmoe_linear_fp8_workspace", "mmoe_linear_fp8", "mmoe_block_norm")
 MAX_CHAIN_LAYERS = 32
 
 F32, BF16 = 0, 1  # element types of the e4m3 operators and the block norm
@@ -61,6 +61,14 @@ class Weights(C.Structure):
     _fields_ = [("w_router", C.c_void_p), ("router_bias", C.c_void_p), ("w_gate_up", C.c_void_p),
                 ("s_gate_up", C.c_void_p), ("w_down", C.c_void_p), ("s_down", C.c_void_p),
                 ("on_device", C.c_int32)]
+
+
+class Norm(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("d", C.c_int32), ("r_type", C.c_int32), ("y_type", C.c_int32),
+                ("gate_col", C.c_int32), ("gate_row", C.c_int64), ("residual_scale", C.c_float), ("eps", C.c_float),
+                ("r", C.c_void_p), ("ldr", C.c_int64), ("y", C.c_void_p), ("ldy", C.c_int64), ("w_post", C.c_void_p),
+                ("gate", C.c_void_p), ("w_pre", C.c_void_p), ("r_out", C.c_void_p), ("ldo", C.c_int64),
+                ("x", C.c_void_p), ("xq", C.c_void_p), ("sx", C.c_void_p)]
 
 
 _lib = None
@@ -98,6 +106,7 @@ def lib() -> C.CDLL:
     L.mmoe_gemm_fp8_grouped.argtypes = [vp, vp, i64, vp, i64, vp, vp, i64, i64, vp, i32, i64, vp]
     L.mmoe_linear_fp8_workspace.argtypes = [i64, i64, C.POINTER(C.c_size_t)]
     L.mmoe_linear_fp8.argtypes = [vp, i64, i64, vp, vp, i64, i64, vp, i32, i64, vp, C.c_size_t, vp]
+    L.mmoe_block_norm.argtypes = [C.POINTER(Norm), vp]
     for name in EXPORTS:
         if name != "mmoe_last_error":
             getattr(L, name).restype = st

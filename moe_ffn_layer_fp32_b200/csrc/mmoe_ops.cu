@@ -1,11 +1,12 @@
 // C entries of the stateless operators (declared in include/mmoe.h): the e4m3
-// quantisers and products.
+// quantisers and products and the block norm.
 #include <cuda_runtime.h>
 
 #include <mutex>
 
 #include "fp8.cuh"
 #include "mmoe_internal.cuh"
+#include "norm.cuh"
 
 using namespace mmoe;
 
@@ -228,6 +229,60 @@ mmoe_status mmoe_linear_fp8(const uint16_t* x_bf16, int64_t M, int64_t ldx, cons
     p.x = nullptr;
     if (e == cudaSuccess) e = f8::launch_product(p, st);
     return e == cudaSuccess ? MMOE_OK : report_cuda(e, "linear launch");
+}
+
+mmoe_status mmoe_block_norm(const mmoe_norm* n, void* stream) {
+    if (!n) return report(MMOE_ERR_INVALID_ARG, "arguments are NULL");
+    CHECK(check_rows(n->rows, "rows"));
+    if (n->d < 8 || n->d > kNormMaxDim || n->d % 8)
+        return report(MMOE_ERR_INVALID_ARG, "d=%d: must be a multiple of 8 in [8, %d]", n->d, kNormMaxDim);
+    CHECK(check_type(n->r_type, "r_type"));
+    CHECK(check_type(n->y_type, "y_type"));
+    if (!(n->eps >= 0.0f)) return report(MMOE_ERR_INVALID_ARG, "eps must not be negative or NaN");
+    if (n->rows == 0) return MMOE_OK;
+    const int64_t rows = n->rows, d = n->d, rs = size_of(n->r_type), ys = size_of(n->y_type), kb = f8::blocks_of(d);
+    if (!n->r) return report(MMOE_ERR_INVALID_ARG, "r is NULL");
+    if (!n->y && (n->w_post || n->gate)) return report(MMOE_ERR_INVALID_ARG, "w_post and gate need y");
+    if ((n->x || n->xq || n->sx) && !n->w_pre) return report(MMOE_ERR_INVALID_ARG, "x, xq and sx need w_pre");
+    if (n->w_pre && !n->x && !n->xq) return report(MMOE_ERR_INVALID_ARG, "w_pre needs x or xq");
+    if (!n->xq != !n->sx) return report(MMOE_ERR_INVALID_ARG, "xq and sx are given together");
+    if (!n->r_out && !n->w_pre) return report(MMOE_ERR_INVALID_ARG, "no output");
+    const struct { const void* p; int64_t ld, size; const char* name; } strided[] = {
+        {n->r, n->ldr, rs, "r"}, {n->y, n->ldy, ys, "y"}, {n->r_out, n->ldo, rs, "r_out"}};
+    for (const auto& t : strided) {
+        if (!t.p) continue;
+        if (t.ld < d || t.ld % (16 / t.size) || !aligned16(t.p))
+            return report(MMOE_ERR_INVALID_ARG, "%s must be 16-byte aligned with rows of at least d elements and whole 16 bytes apart", t.name);
+    }
+    if (n->gate && (n->gate_col != 0 && n->gate_col != 1))
+        return report(MMOE_ERR_INVALID_ARG, "gate_col=%d: must be 0 or 1", n->gate_col);
+    if (n->gate && n->gate_row < 0) return report(MMOE_ERR_INVALID_ARG, "gate_row must not be negative");
+    if (n->gate && (n->gate_col ? (!aligned16(n->gate) || n->gate_row % 4) : reinterpret_cast<uintptr_t>(n->gate) % 4 != 0))
+        return report(MMOE_ERR_INVALID_ARG, "gate: a gate per feature needs 16-byte aligned rows, one per row 4-byte ones");
+    for (const void* p : {(const void*)n->w_post, (const void*)n->w_pre, (const void*)n->x, (const void*)n->xq})
+        if (p && !aligned16(p)) return report(MMOE_ERR_INVALID_ARG, "w_post, w_pre, x and xq must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(n->sx) % 4) return report(MMOE_ERR_INVALID_ARG, "sx must be 4-byte aligned");
+    // every output apart from every other buffer, but r_out may be r itself
+    const struct { const void* p; int64_t bytes; } in[] = {
+        {n->r, ((rows - 1) * n->ldr + d) * rs}, {n->y, n->y ? ((rows - 1) * n->ldy + d) * ys : 0}, {n->w_post, n->w_post ? 4 * d : 0},
+        {n->w_pre, n->w_pre ? 4 * d : 0}, {n->gate, n->gate ? 4 * ((rows - 1) * n->gate_row + (n->gate_col ? d : 1)) : 0}};
+    const struct { const void* p; int64_t bytes; } out[] = {
+        {n->r_out, n->r_out ? ((rows - 1) * n->ldo + d) * rs : 0}, {n->x, n->x ? 2 * rows * d : 0}, {n->xq, n->xq ? rows * d : 0},
+        {n->sx, n->sx ? 4 * rows * kb : 0}};
+    const bool in_place = n->r_out == n->r && n->ldo == n->ldr;
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 5; ++j)
+            if (!(i == 0 && j == 0 && in_place) && overlap(out[i].p, out[i].bytes, in[j].p, in[j].bytes))
+                return report(MMOE_ERR_INVALID_ARG, "an output overlaps an input");
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+                return report(MMOE_ERR_INVALID_ARG, "two outputs overlap");
+    }
+    const NormPlan p = {rows, n->d, n->r, n->ldr, n->r_type == MMOE_BF16, n->y, n->ldy, n->y_type == MMOE_BF16, n->w_post,
+                        n->gate, n->gate_row, n->gate_col, n->residual_scale, n->eps, n->r_out, n->ldo, n->w_pre, n->x,
+                        n->xq, n->sx};
+    const cudaError_t e = launch_block_norm(p, (cudaStream_t)stream);
+    return e == cudaSuccess ? MMOE_OK : report_cuda(e, "block norm launch");
 }
 
 }  // extern "C"
