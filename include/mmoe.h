@@ -443,6 +443,42 @@ mmoe_status mmoe_linear_fp8(const uint16_t* x_bf16, int64_t M, int64_t ldx, cons
                             int64_t K, void* y, int32_t y_type, int64_t ldy, void* workspace, size_t workspace_bytes,
                             void* stream);
 
+/* The MoE layer, Eq. (*), on such weights: FFN(x) = down(Q(silu(gate Q(x)) *
+ * (up Q(x)))), Q the quantisation of a row as above, silu and the products in
+ * FP32, the router (FP32 weights) on x itself; the expert rows are added in
+ * the order of Eq. (*), y = FFN_s + g_0 FFN_0 + ..., so that y is
+ * bit-reproducible.  The config is that of mmoe_create with group_size 128 and
+ * flags 0.  All weights are device pointers, read in place (codes 16-byte
+ * aligned), with KB(n) = ceil(n / 128):
+ *   w_router         FP32 [d, E];  router_bias FP32 [E] or NULL
+ *   w_gate_up        codes [E, 2h, d], gate rows first; s_gate_up FP32 [E, 2 KB(h), KB(d)], the gate
+ *                    rows' blocks first (gate and up are quantised apart: no block holds both)
+ *   w_down           codes [E, d, h]; s_down FP32 [E, KB(d), KB(h)]
+ *   w_shared_*, s_shared_*  the shared expert's, as those of one expert of hidden size shared_hidden */
+typedef struct {
+    const float* w_router;
+    const float* router_bias;
+    const uint8_t* w_gate_up;
+    const float* s_gate_up;
+    const uint8_t* w_down;
+    const float* s_down;
+    const uint8_t* w_shared_gate_up;
+    const float* s_shared_gate_up;
+    const uint8_t* w_shared_down;
+    const float* s_shared_down;
+} mmoe_fp8_weights;
+
+/* y [T, d] (y_type) from x (BF16 [T, d], 16-byte aligned), for T up to
+ * min(64, max_tokens): two launches.  Optional outputs as in mmoe_forward.
+ * The workspace (device, 256-byte aligned, the size that mmoe_fp8_workspace
+ * writes to *bytes) needs no clearing and holds nothing between calls; calls
+ * that may overlap on the GPU, replays of two captured graphs among them, need
+ * one each.  T = 0 is a no-op. */
+mmoe_status mmoe_fp8_workspace(const mmoe_config* cfg, int64_t T, size_t* bytes);
+mmoe_status mmoe_forward_fp8(const mmoe_config* cfg, const mmoe_fp8_weights* w, const uint16_t* x_bf16, int64_t T, void* y,
+                             int32_t y_type, int32_t* topk_idx, float* topk_gate, int32_t* expert_counts,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- between two blocks -----------------------------------------------------
  * The norm after a block, the block's gate, the residual update and the norm
  * before the next block, for every row:

@@ -34,7 +34,8 @@ EXPORTS = ("mmoe_create", "mmoe_load_quantized_weights", "mmoe_forward", "mmoe_f
            "mmoe_profile_enable", "mmoe_profile_read", "mmoe_forward_static_scratch", "mmoe_debug_host_chunks",
            "mmoe_debug_set_wait_limit", "mmoe_debug_fail_alloc", "mmoe_forward_chain",
            "mmoe_quantize_fp8_rows", "mmoe_quantize_fp8_blocks", "mmoe_gemm_fp8", "mmoe_gemm_fp8_grouped",
-           "mmoe_linear_fp8_workspace", "mmoe_linear_fp8", "mmoe_block_norm")
+           "mmoe_linear_fp8_workspace", "mmoe_linear_fp8", "mmoe_fp8_workspace", "mmoe_forward_fp8",
+           "mmoe_block_norm")
 MAX_CHAIN_LAYERS = 32
 
 F32, BF16 = 0, 1  # element types of the e4m3 operators and the block norm
@@ -61,6 +62,11 @@ class Weights(C.Structure):
     _fields_ = [("w_router", C.c_void_p), ("router_bias", C.c_void_p), ("w_gate_up", C.c_void_p),
                 ("s_gate_up", C.c_void_p), ("w_down", C.c_void_p), ("s_down", C.c_void_p),
                 ("on_device", C.c_int32)]
+
+
+class FP8Weights(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("w_router", "router_bias", "w_gate_up", "s_gate_up", "w_down", "s_down",
+                                          "w_shared_gate_up", "s_shared_gate_up", "w_shared_down", "s_shared_down")]
 
 
 class Norm(C.Structure):
@@ -106,6 +112,9 @@ def lib() -> C.CDLL:
     L.mmoe_gemm_fp8_grouped.argtypes = [vp, vp, i64, vp, i64, vp, vp, i64, i64, vp, i32, i64, vp]
     L.mmoe_linear_fp8_workspace.argtypes = [i64, i64, C.POINTER(C.c_size_t)]
     L.mmoe_linear_fp8.argtypes = [vp, i64, i64, vp, vp, i64, i64, vp, i32, i64, vp, C.c_size_t, vp]
+    L.mmoe_fp8_workspace.argtypes = [C.POINTER(Config), i64, C.POINTER(C.c_size_t)]
+    L.mmoe_forward_fp8.argtypes = [C.POINTER(Config), C.POINTER(FP8Weights), vp, i64, vp, i32, vp, vp, vp, vp, C.c_size_t,
+                                   vp]
     L.mmoe_block_norm.argtypes = [C.POINTER(Norm), vp]
     for name in EXPORTS:
         if name != "mmoe_last_error":

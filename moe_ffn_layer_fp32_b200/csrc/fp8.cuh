@@ -149,6 +149,33 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort_
     }
 }
 
+// Signals an mbarrier of a peer CTA (this thread's earlier stores, and what it has seen of others', come before),
+// and the bounded wait for such signals.
+__device__ __forceinline__ void peer_arrive(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int* abort_word, int* err, int site) {
+    const long long t0 = async::clk();
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(async::su32(bar)), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if (*reinterpret_cast<volatile int*>(abort_word)) return false;
+        if (async::clk() - t0 > kWaitClk) {
+            atomicExch(abort_word, 1);
+            *reinterpret_cast<volatile int*>(err) = site;
+            __threadfence_system();
+            return false;
+        }
+    }
+}
+
 // One lane waits, the warp follows.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort_word, int* err, int site) {
     bool ok = true;

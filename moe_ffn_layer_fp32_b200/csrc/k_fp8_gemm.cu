@@ -215,10 +215,10 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
         tc5::tmem_alloc(&sm->tmem, kBufs * H * kBlk);
         tc5::before_sync();
     }
-    dep_launch();
     dep_wait();
     __syncthreads();
     tc5::after_sync();
+    dep_launch();  // not before this CTA has its TMEM: a dependent that waits for this grid may take the rest
     const uint32_t tmem = sm->tmem;
 
     if (warp < 4) {
@@ -448,10 +448,10 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
         tc5::tmem_alloc(&sm->tmem, kCols);
         tc5::before_sync();
     }
-    dep_launch();
     dep_wait();
     __syncthreads();
     tc5::after_sync();
+    dep_launch();  // not before this CTA has its TMEM: a dependent that waits for this grid may take the rest
     const uint32_t tmem = sm->tmem;
     const int m = (int)p.M;
 

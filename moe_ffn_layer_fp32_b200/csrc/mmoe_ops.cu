@@ -1,10 +1,11 @@
 // C entries of the stateless operators (declared in include/mmoe.h): the e4m3
-// quantisers and products and the block norm.
+// quantisers, products and MoE layer, and the block norm.
 #include <cuda_runtime.h>
 
 #include <mutex>
 
 #include "fp8.cuh"
+#include "fp8_moe.cuh"
 #include "mmoe_internal.cuh"
 #include "norm.cuh"
 
@@ -114,6 +115,48 @@ mmoe_status check_codes(const uint8_t* a, const float* sa, int64_t M, int64_t K,
 // mmoe_linear_fp8's workspace: the scales, then the codes of x.
 size_t scale_bytes(int64_t M, int64_t K) { return (size_t)(M * f8::blocks_of(K) * 4 + 15) / 16 * 16; }
 size_t linear_workspace(int64_t M, int64_t K) { return M <= f8::kSmallRows ? 0 : scale_bytes(M, K) + (size_t)(M * K); }
+
+mmoe_status check_fp8_config(const mmoe_config* c) {
+    if (!c) return report(MMOE_ERR_INVALID_ARG, "config is NULL");
+    if (c->d_model < 64 || c->d_model > 8192 || c->d_model % 32)
+        return report(MMOE_ERR_INVALID_ARG, "d_model=%d: must be a multiple of 32 in [64, 8192]", c->d_model);
+    if (c->n_experts < 1 || c->n_experts > kMaxExperts)
+        return report(MMOE_ERR_INVALID_ARG, "n_experts=%d: must be in [1, %d]", c->n_experts, kMaxExperts);
+    if (c->top_k < 1 || c->top_k > c->n_experts || c->top_k > kMaxTopK)
+        return report(MMOE_ERR_INVALID_ARG, "top_k=%d: must be in [1, min(n_experts, %d)]", c->top_k, kMaxTopK);
+    if (c->expert_hidden < 32 || c->expert_hidden > 4096 || c->expert_hidden % 32)
+        return report(MMOE_ERR_INVALID_ARG, "expert_hidden=%d: must be a multiple of 32 in [32, 4096]", c->expert_hidden);
+    if (c->shared_hidden < 32 || c->shared_hidden > 4096 || c->shared_hidden % 32)
+        return report(MMOE_ERR_INVALID_ARG, "shared_hidden=%d: must be a multiple of 32 in [32, 4096]", c->shared_hidden);
+    if (c->group_size != f8::kBlk) return report(MMOE_ERR_INVALID_ARG, "group_size=%d: must be 128", c->group_size);
+    if (c->max_tokens < 1 || c->max_tokens > (1 << 20))
+        return report(MMOE_ERR_INVALID_ARG, "max_tokens=%d: must be in [1, 2^20]", c->max_tokens);
+    if (c->gating != MMOE_GATE_SOFTMAX && c->gating != MMOE_GATE_SIGMOID_TOPK_NORM &&
+        c->gating != MMOE_GATE_SIGMOID_TOPK_NORM_SEL_BIAS)
+        return report(MMOE_ERR_INVALID_ARG, "gating=%d: unknown", c->gating);
+    if (c->has_router_bias != 0 && c->has_router_bias != 1)
+        return report(MMOE_ERR_INVALID_ARG, "has_router_bias=%d: must be 0 or 1", c->has_router_bias);
+    if (c->flags) return report(MMOE_ERR_INVALID_ARG, "flags=0x%x: must be 0", c->flags);
+    return MMOE_OK;
+}
+
+mmoe_status check_tokens(const mmoe_config* c, int64_t T) {
+    const int64_t most = c->max_tokens < f8::kFewTokens ? c->max_tokens : f8::kFewTokens;
+    if (T < 0 || T > most) return report(MMOE_ERR_INVALID_ARG, "T=%lld: must be in [0, %lld]", (long long)T, (long long)most);
+    return MMOE_OK;
+}
+
+f8::MoePlan moe_plan(const mmoe_config* c, int64_t T) {
+    f8::MoePlan p = {};
+    p.d = c->d_model;
+    p.h = c->expert_hidden;
+    p.hs = c->shared_hidden;
+    p.E = c->n_experts;
+    p.k = c->top_k;
+    p.gating = c->gating;
+    p.T = (int)T;
+    return p;
+}
 
 }  // namespace
 
@@ -229,6 +272,77 @@ mmoe_status mmoe_linear_fp8(const uint16_t* x_bf16, int64_t M, int64_t ldx, cons
     p.x = nullptr;
     if (e == cudaSuccess) e = f8::launch_product(p, st);
     return e == cudaSuccess ? MMOE_OK : report_cuda(e, "linear launch");
+}
+
+mmoe_status mmoe_fp8_workspace(const mmoe_config* cfg, int64_t T, size_t* bytes) {
+    if (!bytes) return report(MMOE_ERR_INVALID_ARG, "bytes is NULL");
+    CHECK(check_fp8_config(cfg));
+    CHECK(check_tokens(cfg, T));
+    f8::MoePlan p = moe_plan(cfg, T);
+    *bytes = T ? f8::carve_moe(p, nullptr) : 0;
+    return MMOE_OK;
+}
+
+mmoe_status mmoe_forward_fp8(const mmoe_config* cfg, const mmoe_fp8_weights* w, const uint16_t* x_bf16, int64_t T, void* y,
+                             int32_t y_type, int32_t* topk_idx, float* topk_gate, int32_t* expert_counts,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+    CHECK(check_fp8_config(cfg));
+    CHECK(check_tokens(cfg, T));
+    CHECK(check_type(y_type, "y_type"));
+    if (!w) return report(MMOE_ERR_INVALID_ARG, "weights is NULL");
+    f8::MoePlan p = moe_plan(cfg, T);
+    const int64_t d = p.d, h = p.h, hs = p.hs, E = p.E, k = p.k, db = f8::blocks_of(d), hb = f8::blocks_of(h), sb = f8::blocks_of(hs);
+    const struct { const void* p; int64_t bytes; bool codes; } in[] = {
+        {w->w_router, 4 * d * E, false}, {w->w_gate_up, E * 2 * h * d, true}, {w->s_gate_up, 4 * E * 2 * hb * db, false},
+        {w->w_down, E * d * h, true}, {w->s_down, 4 * E * db * hb, false}, {w->w_shared_gate_up, 2 * hs * d, true},
+        {w->s_shared_gate_up, 4 * 2 * sb * db, false}, {w->w_shared_down, d * hs, true}, {w->s_shared_down, 4 * db * sb, false}};
+    for (const auto& t : in) {
+        if (!t.p) return report(MMOE_ERR_INVALID_ARG, "a weight pointer is NULL");
+        if (t.codes ? !aligned16(t.p) : reinterpret_cast<uintptr_t>(t.p) % 4 != 0)
+            return report(MMOE_ERR_INVALID_ARG, "weight codes must be 16-byte, other weights 4-byte aligned");
+    }
+    if (cfg->has_router_bias && !w->router_bias)
+        return report(MMOE_ERR_INVALID_ARG, "the config has a router bias but router_bias is NULL");
+    if (reinterpret_cast<uintptr_t>(w->router_bias) % 4) return report(MMOE_ERR_INVALID_ARG, "router_bias must be 4-byte aligned");
+    if (T == 0) return MMOE_OK;
+    if (!x_bf16 || !y) return report(MMOE_ERR_INVALID_ARG, "x or y is NULL");
+    if (!aligned16(x_bf16) || reinterpret_cast<uintptr_t>(y) % size_of(y_type))
+        return report(MMOE_ERR_INVALID_ARG, "x must be 16-byte aligned, y aligned to its elements");
+    for (const void* o : {(const void*)topk_idx, (const void*)topk_gate, (const void*)expert_counts})
+        if (reinterpret_cast<uintptr_t>(o) % 4) return report(MMOE_ERR_INVALID_ARG, "optional outputs must be 4-byte aligned");
+    const size_t need = f8::carve_moe(p, nullptr);
+    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < need)
+        return report(MMOE_ERR_INVALID_ARG, "the workspace must be 256-byte aligned and %zu bytes long", need);
+    const struct { const void* p; int64_t bytes; } out[] = {
+        {y, T * d * size_of(y_type)}, {topk_idx, topk_idx ? 4 * T * k : 0}, {topk_gate, topk_gate ? 4 * T * k : 0},
+        {expert_counts, expert_counts ? 4 * (E + 1) : 0}, {workspace, (int64_t)need}};
+    for (int i = 0; i < 5; ++i) {
+        bool bad = overlap(out[i].p, out[i].bytes, x_bf16, T * d * 2) ||
+                   (cfg->has_router_bias && overlap(out[i].p, out[i].bytes, w->router_bias, 4 * E));
+        for (const auto& t : in) bad = bad || overlap(out[i].p, out[i].bytes, t.p, t.bytes);
+        for (int j = 0; j < i; ++j) bad = bad || overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes);
+        if (bad) return report(MMOE_ERR_INVALID_ARG, "an output or the workspace overlaps another buffer");
+    }
+    CHECK(device_flag(&p.err));
+    f8::carve_moe(p, static_cast<unsigned char*>(workspace));
+    p.w_router = w->w_router;
+    p.router_bias = cfg->has_router_bias ? w->router_bias : nullptr;
+    p.gate_up = w->w_gate_up;
+    p.s_gate_up = w->s_gate_up;
+    p.down = w->w_down;
+    p.s_down = w->s_down;
+    p.sh_gate_up = w->w_shared_gate_up;
+    p.sh_s_gate_up = w->s_shared_gate_up;
+    p.sh_down = w->w_shared_down;
+    p.sh_s_down = w->s_shared_down;
+    p.x = reinterpret_cast<const __nv_bfloat16*>(x_bf16);
+    p.y = y;
+    p.y_bf16 = y_type == MMOE_BF16;
+    p.out_idx = topk_idx;
+    p.out_gate = topk_gate;
+    p.out_counts = expert_counts;
+    const cudaError_t e = f8::launch_moe_few(p, (cudaStream_t)stream);
+    return e == cudaSuccess ? MMOE_OK : report_cuda(e, "MoE layer launch");
 }
 
 mmoe_status mmoe_block_norm(const mmoe_norm* n, void* stream) {

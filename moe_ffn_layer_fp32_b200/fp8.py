@@ -1,4 +1,5 @@
-"""8-bit floating-point (e4m3) operators with one FP32 scale per block of 128: quantisers and matrix products.
+"""8-bit floating-point (e4m3) operators with one FP32 scale per block of 128: quantisers, matrix products and the MoE
+layer on such weights.
 
 Thin wrappers over the C ABI (include/mmoe.h): PyTorch provides device memory and streams, every step runs in
 libmmoe.so.  Codes are ``torch.float8_e4m3fn`` tensors.  A tensor allocated here belongs to ``stream`` (the current
@@ -10,6 +11,7 @@ import ctypes as C
 
 import torch
 
+from . import _lib
 from ._lib import check, lib
 from ._tensors import E4M3, TYPE, blocks, need, on, row_stride, rows_of, same_device
 
@@ -134,3 +136,87 @@ def linear_fp8(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor, y: torch.Ten
         check(lib().mmoe_linear_fp8(x.data_ptr(), M, row_stride(x), wq.data_ptr(), sw.data_ptr(), N, K, y.data_ptr(),
                                     TYPE[y.dtype], row_stride(y), at, size, st))
     return y
+
+
+def _optional(t: torch.Tensor | None, shape, dtype, name: str):
+    if t is None:
+        return None
+    need(t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous(), f"{name} must be contiguous {dtype} of shape {shape}")
+    return t.data_ptr()
+
+
+class FP8MoELayer:
+    """The MoE feed-forward layer (Eq. (*) of the MobileMoE pages) on e4m3 weights, for up to 64 tokens a call.
+
+    ``load`` keeps the caller's tensors and reads them in place; every ``forward`` allocates its own workspace, so that
+    calls on several streams, and captured graphs, do not share one."""
+
+    def __init__(self, d_model: int, expert_hidden: int, *, shared_hidden: int | None = None, n_experts: int = 60,
+                 top_k: int = 4, max_tokens: int = 64, gating: int = 0, has_router_bias: bool = False):
+        self.cfg = _lib.Config(d_model, n_experts, top_k, expert_hidden,
+                               expert_hidden if shared_hidden is None else shared_hidden, 128, max_tokens, gating,
+                               int(has_router_bias), 0)
+        self._keep = None
+        self._room: dict[int, int] = {}  # workspace bytes for a number of tokens
+        self._workspace_bytes(0)         # checks the config
+
+    @property
+    def d_model(self) -> int:
+        return self.cfg.d_model
+
+    def _workspace_bytes(self, T: int) -> int:
+        if T not in self._room:
+            n = C.c_size_t()
+            check(lib().mmoe_fp8_workspace(C.byref(self.cfg), T, C.byref(n)))
+            self._room[T] = n.value
+        return self._room[T]
+
+    def load(self, w_router, router_bias, w_gate_up, s_gate_up, w_down, s_down, w_shared_gate_up, s_shared_gate_up,
+             w_shared_down, s_shared_down) -> None:
+        """Weights in the layout of include/mmoe.h (mmoe_fp8_weights), contiguous CUDA tensors on one device."""
+        c = self.cfg
+        d, h, hs, E = c.d_model, c.expert_hidden, c.shared_hidden, c.n_experts
+        need((router_bias is not None) == bool(c.has_router_bias), "router_bias must be given exactly where the layer has one")
+        for t, shape, dtype, name in (
+                (w_router, (d, E), torch.float32, "w_router"), (router_bias, (E,), torch.float32, "router_bias"),
+                (w_gate_up, (E, 2 * h, d), E4M3, "w_gate_up"), (w_down, (E, d, h), E4M3, "w_down"),
+                (s_gate_up, (E, 2 * blocks(h), blocks(d)), torch.float32, "s_gate_up"),
+                (s_down, (E, blocks(d), blocks(h)), torch.float32, "s_down"),
+                (w_shared_gate_up, (2 * hs, d), E4M3, "w_shared_gate_up"), (w_shared_down, (d, hs), E4M3, "w_shared_down"),
+                (s_shared_gate_up, (2 * blocks(hs), blocks(d)), torch.float32, "s_shared_gate_up"),
+                (s_shared_down, (blocks(d), blocks(hs)), torch.float32, "s_shared_down")):
+            need(t is not None or name == "router_bias", f"{name} must be given")
+            _optional(t, shape, dtype, name)
+        keep = (w_router, router_bias, w_gate_up, s_gate_up, w_down, s_down, w_shared_gate_up, s_shared_gate_up,
+                w_shared_down, s_shared_down)
+        same_device(*keep)
+        self._keep = keep
+        self._weights = _lib.FP8Weights(*[None if t is None else t.data_ptr() for t in keep])
+
+    def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, *, out_dtype: torch.dtype = torch.float32, stream=None,
+                topk_idx=None, topk_gate=None, expert_counts=None) -> torch.Tensor:
+        """y [T, d] (given, or new of out_dtype: float32 or bfloat16) from x [T, d] (bfloat16, contiguous)."""
+        c = self.cfg
+        d, k = c.d_model, c.top_k
+        need(self._keep is not None, "the layer has no weights: call load() first")
+        need(x.dtype == torch.bfloat16 and x.dim() == 2 and x.shape[1] == d and x.is_contiguous(),
+             "x must be a contiguous [T, d_model] bfloat16 tensor")
+        T = x.shape[0]
+        out = (_optional(topk_idx, (T, k), torch.int32, "topk_idx"), _optional(topk_gate, (T, k), torch.float32, "topk_gate"),
+               _optional(expert_counts, (c.n_experts + 1,), torch.int32, "expert_counts"))
+        same_device(x, self._keep[0], y, topk_idx, topk_gate, expert_counts)
+        room = self._workspace_bytes(T)
+        ctx, st = on(x, stream)
+        with ctx:
+            if y is None:
+                need(out_dtype in TYPE, "out_dtype must be float32 or bfloat16")
+                y = torch.empty((T, d), dtype=out_dtype, device=x.device)
+            else:
+                need(y.dtype in TYPE and tuple(y.shape) == (T, d) and y.is_contiguous(),
+                     "y must be a contiguous [T, d_model] float32 or bfloat16 tensor")
+            space = torch.empty(room, dtype=torch.uint8, device=x.device)
+            check(lib().mmoe_forward_fp8(C.byref(c), C.byref(self._weights), x.data_ptr(), T, y.data_ptr(), TYPE[y.dtype],
+                                         *out, space.data_ptr(), room, st))
+        return y
+
+    __call__ = forward
