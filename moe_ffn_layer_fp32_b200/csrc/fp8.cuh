@@ -176,13 +176,33 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int
     }
 }
 
-// One lane waits, the warp follows.
+// The same by a whole warp, which decides as one.  Every lane polls: against one lane that polls and a shuffle that
+// tells the others, a block of 128 of the promotion loops took 639 instead of 1042 clocks.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort_word, int* err, int site) {
-    bool ok = true;
-    if ((threadIdx.x & 31) == 0) ok = wait(bar, parity, abort_word, err, site);
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    __syncwarp();
-    return ok;
+    if (__all_sync(0xffffffffu, async::mbar_try_wait(bar, parity))) return true;
+    const long long t0 = async::clk();
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (__all_sync(0xffffffffu, async::mbar_try_wait(bar, parity))) return true;
+        const bool late = async::clk() - t0 > kWaitClk;
+        if (late) {
+            atomicExch(abort_word, 1);
+            *reinterpret_cast<volatile int*>(err) = site;
+            __threadfence_system();
+        }
+        if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile int*>(abort_word))) return false;
+    }
+}
+
+// One lane of a converged warp, the same each time.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 
 // The wait used while draining: ignores the abort word.

@@ -231,47 +231,52 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
             } else {
                 total = (p.M + kBlk - 1) / kBlk * ntiles;
             }
-            if (lane == 0) {
-                int sc = 0, tc = 0;
-                bool ok = true;
-                for (int64_t L = blockIdx.x; ok; L += gridDim.x, ++tc) {
-                    const int b = tc % kTInfo;
-                    if (tc >= kTInfo && !wait(&sm->tempty[b], (tc / kTInfo - 1) & 1, &sm->abort, p.err, 1)) break;
-                    TileInfo& ti = sm->ti[b];
-                    const bool last = L >= total;
-                    ti.end = last;
-                    if (last) {
+            int sc = 0, tc = 0;
+            bool ok = true;
+            for (int64_t L = blockIdx.x; ok; L += gridDim.x, ++tc) {
+                const int b = tc % kTInfo;
+                if (tc >= kTInfo && !warp_wait(&sm->tempty[b], (tc / kTInfo - 1) & 1, &sm->abort, p.err, 1)) break;
+                TileInfo& ti = sm->ti[b];
+                if (L >= total) {
+                    if (lane == 0) {
+                        ti.end = 1;
                         mbar_arrive(&sm->tfull[b]);
-                        break;
                     }
-                    // column tiles innermost: the CTAs that run together share activation tiles in L2
-                    const int64_t mt = L / ntiles;
-                    const int nt = (int)(L - mt * ntiles);
-                    int g = 0;
-                    int64_t row0 = mt * kBlk, rows = p.M;
-                    if (p.groups) {
-                        int lo = 0, hi = p.groups - 1;  // the last group with tiles[g] <= mt
-                        while (lo < hi) {
-                            const int mid = (lo + hi + 1) >> 1;
-                            if (sm->tiles[mid] <= mt) lo = mid;
-                            else hi = mid - 1;
-                        }
-                        g = lo;
-                        row0 = sm->off[g] + (mt - sm->tiles[g]) * kBlk;
-                        rows = sm->off[g + 1];
+                    break;
+                }
+                // column tiles innermost: the CTAs that run together share activation tiles in L2
+                const int64_t mt = L / ntiles;
+                const int nt = (int)(L - mt * ntiles);
+                int g = 0;
+                int64_t row0 = mt * kBlk, rows = p.M;
+                if (p.groups) {
+                    int lo = 0, hi = p.groups - 1;  // the last group with tiles[g] <= mt
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) >> 1;
+                        if (sm->tiles[mid] <= mt) lo = mid;
+                        else hi = mid - 1;
                     }
+                    g = lo;
+                    row0 = sm->off[g] + (mt - sm->tiles[g]) * kBlk;
+                    rows = sm->off[g + 1];
+                }
+                const int n0 = nt * H * kBlk;
+                if (lane == 0) {
+                    ti.end = 0;
                     ti.nr = (int)min((int64_t)kBlk, rows - row0);
-                    ti.n0 = nt * H * kBlk;
+                    ti.n0 = n0;
                     ti.sw0 = (g * nb + nt * H) * KB;
                     ti.row0 = row0;
                     mbar_arrive(&sm->tfull[b]);
-                    const int w0 = g * p.N + ti.n0;
-                    for (int kb = 0; kb < KB; ++kb, ++sc) {
-                        const int s = sc % S;
-                        if (sc >= S && !wait(&sm->empty[s], (sc / S - 1) & 1, &sm->abort, p.err, 2)) {
-                            ok = false;
-                            break;
-                        }
+                }
+                const int w0 = g * p.N + n0;
+                for (int kb = 0; kb < KB; ++kb, ++sc) {
+                    const int s = sc % S;
+                    if (sc >= S && !warp_wait(&sm->empty[s], (sc / S - 1) & 1, &sm->abort, p.err, 2)) {
+                        ok = false;
+                        break;
+                    }
+                    if (elect()) {
                         mbar_expect_tx(&sm->full[s], kTx);
                         tc5::tma_load_2d(sm->ring[s], &amap, kb * kBlk, (int)row0, &sm->full[s]);
 #pragma unroll
@@ -279,24 +284,28 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                             tc5::tma_load_2d(sm->ring[s] + (1 + h) * kTileBytes, &wmap, kb * kBlk, w0 + h * kBlk,
                                              &sm->full[s]);
                     }
+                    __syncwarp();
                 }
-                // every copy has landed before the CTA may exit
-                for (int i = max(sc - S, 0); i < sc; ++i) wait_drain(&sm->full[i % S], (i / S) & 1);
             }
-        } else if (warp == 1 && lane == 0) {
+            // every copy has landed before the CTA may exit
+            for (int i = max(sc - S, 0); i < sc; ++i) wait_drain(&sm->full[i % S], (i / S) & 1);
+        } else if (warp == 1) {
+            // the warp walks together and one lane issues: in a branch of one lane the same loop starves beside the
+            // promotion warps
             int sc = 0, tc = 0;
             bool ok = true;
             while (ok) {
                 const int b = tc % kTInfo;
-                if (!wait(&sm->tfull[b], (tc / kTInfo) & 1, &sm->abort, p.err, 3)) break;
+                if (!warp_wait(&sm->tfull[b], (tc / kTInfo) & 1, &sm->abort, p.err, 3)) break;
                 const int end = sm->ti[b].end;
-                mbar_arrive(&sm->tempty[b]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->tempty[b]);
                 ++tc;
                 if (end) break;
                 for (int kb = 0; kb < KB; ++kb, ++sc) {
                     const int s = sc % S, d = sc % kBufs;
-                    if (!wait(&sm->full[s], (sc / S) & 1, &sm->abort, p.err, 4) ||
-                        !wait(&sm->acce[d], (sc / kBufs) & 1, &sm->abort, p.err, 5)) {
+                    if (!warp_wait(&sm->full[s], (sc / S) & 1, &sm->abort, p.err, 4) ||
+                        !warp_wait(&sm->acce[d], (sc / kBufs) & 1, &sm->abort, p.err, 5)) {
                         ok = false;
                         break;
                     }
@@ -304,11 +313,14 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                     const uint64_t ad = tc5::smem_desc_sw128(sm->ring[s]);
                     const uint64_t wd = tc5::smem_desc_sw128(sm->ring[s] + kTileBytes);
                     const uint32_t dt = tmem + d * H * kBlk;
+                    if (elect()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)  // 32 of K (32 bytes, 2 descriptor units) each
-                        mma_e4m3(dt, ad + 2 * k, wd + 2 * k, idesc_e4m3(H * kBlk), k > 0);
-                    tc5::commit(&sm->empty[s]);
-                    tc5::commit(&sm->accf[d]);
+                        for (int k = 0; k < 4; ++k)  // 32 of K (32 bytes, 2 descriptor units) each
+                            mma_e4m3(dt, ad + 2 * k, wd + 2 * k, idesc_e4m3(H * kBlk), k > 0);
+                        tc5::commit(&sm->empty[s]);
+                        tc5::commit(&sm->accf[d]);
+                    }
+                    __syncwarp();
                 }
             }
             // every MMA has completed before TMEM is released
@@ -370,12 +382,12 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sm->acce[d]);
                     }
-                    const float2 s2 = make_float2(s[i >> 1], s[i >> 1]);
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        acc[i >> 1][(i & 1) * 16 + c] =
-                            __ffma2_rn(make_float2(__uint_as_float(v[i & 1][2 * c]), __uint_as_float(v[i & 1][2 * c + 1])),
-                                       s2, acc[i >> 1][(i & 1) * 16 + c]);
+                    for (int c = 0; c < 16; ++c) {
+                        float2& to = acc[i >> 1][(i & 1) * 16 + c];
+                        to.x = fmaf(__uint_as_float(v[i & 1][2 * c]), s[i >> 1], to.x);
+                        to.y = fmaf(__uint_as_float(v[i & 1][2 * c + 1]), s[i >> 1], to.y);
+                    }
                 }
             }
             if (!ok || *reinterpret_cast<volatile int*>(&sm->abort)) break;
@@ -467,25 +479,26 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
             for (int j = max(i - kRing, 0); j < i; ++j) wait_drain(&sm->full[j % kRing], (j / kRing) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int i = 0;
-            for (; i < mine; ++i) {
-                const int s = i % kRing, d = i % kSBufs, r = i % kRound;
-                if (r == 0 && !wait(&sm->ready, (i / kRound) & 1, &sm->abort, p.err, 12)) break;
-                if (!wait(&sm->full[s], (i / kRing) & 1, &sm->abort, p.err, 13) ||
-                    !wait(&sm->acce[d], (i / kSBufs) & 1, &sm->abort, p.err, 14))
-                    break;
-                tc5::after_sync();
-                const uint64_t wd = tc5::smem_desc_sw128(sm->ring[s]);
-                const uint64_t bd = tc5::smem_desc_sw128(sm->b + r * NT * kBlk);
+        int i = 0;
+        for (; i < mine; ++i) {
+            const int s = i % kRing, d = i % kSBufs, r = i % kRound;
+            if (r == 0 && !warp_wait(&sm->ready, (i / kRound) & 1, &sm->abort, p.err, 12)) break;
+            if (!warp_wait(&sm->full[s], (i / kRing) & 1, &sm->abort, p.err, 13) ||
+                !warp_wait(&sm->acce[d], (i / kSBufs) & 1, &sm->abort, p.err, 14))
+                break;
+            tc5::after_sync();
+            const uint64_t wd = tc5::smem_desc_sw128(sm->ring[s]);
+            const uint64_t bd = tc5::smem_desc_sw128(sm->b + r * NT * kBlk);
+            if (elect()) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     mma_e4m3(tmem + d * NT, wd + 2 * k, bd + 2 * k, idesc_e4m3(NT), k > 0);
                 tc5::commit(&sm->empty[s]);
                 tc5::commit(&sm->accf[d]);
             }
-            if (i > 0) wait_drain(&sm->accf[(i - 1) % kSBufs], ((i - 1) / kSBufs) & 1);
+            __syncwarp();
         }
+        if (i > 0) wait_drain(&sm->accf[(i - 1) % kSBufs], ((i - 1) / kSBufs) & 1);
     } else {
         const int pt = tid - 64, quarter = warp & 3;
         const int row = quarter * 32 + lane;  // weight row of the tile

@@ -355,27 +355,28 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
             for (int j = max(i - lay.ring, 0); j < i; ++j) wait_drain(&sm->full[j % lay.ring], (j / lay.ring) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int i = 0;
-            for (; i < steps; ++i) {
-                const int s = i % lay.ring, b = i % kBufs;
-                if ((i == 0 && gt > 0 && !wait(&sm->xready, 0, &sm->abort, p.err, 22)) ||
-                    (i == ngu && !wait(&sm->hready, 0, &sm->abort, p.err, 23)) ||
-                    !wait(&sm->full[s], (i / lay.ring) & 1, &sm->abort, p.err, 24) ||
-                    !wait(&sm->acce[b], (i / kBufs) & 1, &sm->abort, p.err, 25))
-                    break;
-                tc5::after_sync();
-                const int kb = i < ngu ? i % KBd : (i - ngu) % KBh;
-                const uint64_t wd = tc5::smem_desc_sw128(base + s * kSlot);
-                const uint64_t bd = tc5::smem_desc_sw128(operand + kb * kN * kBlk);
+        int i = 0;
+        for (; i < steps; ++i) {
+            const int s = i % lay.ring, b = i % kBufs;
+            if ((i == 0 && gt > 0 && !warp_wait(&sm->xready, 0, &sm->abort, p.err, 22)) ||
+                (i == ngu && !warp_wait(&sm->hready, 0, &sm->abort, p.err, 23)) ||
+                !warp_wait(&sm->full[s], (i / lay.ring) & 1, &sm->abort, p.err, 24) ||
+                !warp_wait(&sm->acce[b], (i / kBufs) & 1, &sm->abort, p.err, 25))
+                break;
+            tc5::after_sync();
+            const int kb = i < ngu ? i % KBd : (i - ngu) % KBh;
+            const uint64_t wd = tc5::smem_desc_sw128(base + s * kSlot);
+            const uint64_t bd = tc5::smem_desc_sw128(operand + kb * kN * kBlk);
+            if (elect()) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     mma_e4m3(tmem + b * kN, wd + 2 * k, bd + 2 * k, idesc_e4m3(kN), k > 0);
                 tc5::commit(&sm->empty[s]);
                 tc5::commit(&sm->accf[b]);
             }
-            if (i > 0) wait_drain(&sm->accf[(i - 1) % kBufs], ((i - 1) / kBufs) & 1);
+            __syncwarp();
         }
+        if (i > 0) wait_drain(&sm->accf[(i - 1) % kBufs], ((i - 1) / kBufs) & 1);
     } else {
         const int pt = tid - 64, quarter = warp & 3, hl = pt & 15;
         const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
