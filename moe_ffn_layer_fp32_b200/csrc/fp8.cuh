@@ -49,9 +49,39 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-__device__ __forceinline__ uint32_t e4m3x4(const float* v, float s) {
-    return e4m3x2(coded(v[0], s), coded(v[1], s)) | (e4m3x2(coded(v[2], s), coded(v[3], s)) << 16);
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) { return e4m3x2(a, b) | (e4m3x2(c, d) << 16); }
+
+// The codes of a block's values, e4m3(v / s), without a division for each.  hi and lo are 1 / s moved up and down by
+// 2^-21: rcp.approx is off by 2^-23 at most, each product rounds by 2^-24, so v * lo and v * hi lie on either side of
+// the FP32 quotient, and where they have the same code it is the quotient's.  Where they do not (a rounding border
+// within 2^-21, about one value in 10^5), or 1 / s is not a normal number (s zero, tiny, huge, NaN or infinite), the
+// values are divided.  Quantising 32768 x 2048 BF16 values took 106 us with the divisions, and takes 37 us.
+// The divisions are a call: inlined they are most of a kernel's code, and a kernel of a few microseconds waits for its code.
+static __device__ __noinline__ uint2 divided8(float a, float b, float c, float d, float e, float f, float g, float h, float s) {
+    return make_uint2(e4m3x4(coded(a, s), coded(b, s), coded(c, s), coded(d, s)),
+                      e4m3x4(coded(e, s), coded(f, s), coded(g, s), coded(h, s)));
 }
+
+struct Coder {
+    float s, hi, lo;
+    bool fast;
+    __device__ __forceinline__ explicit Coder(float scale) : s(scale) {
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale));
+        fast = scale >= 0x1p-120f && scale <= 0x1p120f;
+        hi = r * (1.0f + 0x1p-21f);
+        lo = r * (1.0f - 0x1p-21f);
+    }
+    __device__ __forceinline__ uint2 operator()(const float (&v)[8]) const {
+        uint2 h, l;
+        h.x = e4m3x4(v[0] * hi, v[1] * hi, v[2] * hi, v[3] * hi);
+        h.y = e4m3x4(v[4] * hi, v[5] * hi, v[6] * hi, v[7] * hi);
+        l.x = e4m3x4(v[0] * lo, v[1] * lo, v[2] * lo, v[3] * lo);
+        l.y = e4m3x4(v[4] * lo, v[5] * lo, v[6] * lo, v[7] * lo);
+        if (!fast || h.x != l.x || h.y != l.y) h = divided8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], s);
+        return h;
+    }
+};
 
 // Ordinary loads: the read-only path may be hoisted above dep_wait.
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
@@ -106,6 +136,52 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// The same for a pair of CTAs (M = 256, 128 rows and half of N in each one's shared memory, at the same addresses),
+// issued in the pair's CTA 0.
+__host__ __device__ constexpr uint32_t idesc_e4m3_pair(int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives on both CTAs' `bar` when the pair operations issued before have completed.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            async::su32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// A tile into this CTA's shared memory, counted on a barrier (a cluster address) of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(async::su32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+// A tile from shared memory to global memory (one group of the issuing thread's).
+__device__ __forceinline__ void tma_store_2d(const void* map, const void* src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(async::su32(src))
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(async::su32(dst_smem)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t tmem, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
 }
 
 // Makes this thread's shared-memory stores visible to the tensor cores and the copy engine.
@@ -192,6 +268,34 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* a
         }
         if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile int*>(abort_word))) return false;
     }
+}
+
+// Signals an mbarrier of a CTA of the cluster that this thread's tensor-memory loads are done (tcgen05.wait::ld and
+// before_sync come first).  It orders nothing else: a release at cluster scope waits for the thread's stores, and made
+// a block of 128 of the product take 2200 clocks.
+__device__ __forceinline__ void peer_arrive_read(uint32_t addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// Both of two barriers.
+__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, int* abort_word, int* err,
+                                           int site) {
+    const bool first = async::mbar_try_wait(a, pa), both = async::mbar_try_wait(b, pb) && first;
+    if (__all_sync(0xffffffffu, both)) return true;
+    return warp_wait(a, pa, abort_word, err, site) && warp_wait(b, pb, abort_word, err, site);
+}
+
+// Whether the phase is complete, without waiting for it (mbar_try_wait may hold the thread for a while).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(async::su32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // One lane of a converged warp, the same each time.

@@ -31,7 +31,9 @@
 namespace mmoe {
 namespace f8 {
 
-cudaError_t byte_map(void* map, const void* base, uint64_t cols, uint64_t rows, uint64_t stride, int box_rows) {
+namespace {
+cudaError_t encode_map(void* map, CUtensorMapDataType type, const void* base, uint64_t cols, uint64_t rows, uint64_t stride,
+                       int box_cols, int box_rows) {
     static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -43,12 +45,22 @@ cudaError_t byte_map(void* map, const void* base, uint64_t cols, uint64_t rows, 
     if (!encode) return cudaErrorNotSupported;
     const cuuint64_t dims[2] = {cols, rows};
     const cuuint64_t strides[1] = {stride};
-    const cuuint32_t box[2] = {(cuuint32_t)kBlk, (cuuint32_t)box_rows};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = encode(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base),
-                              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = encode(static_cast<CUtensorMap*>(map), type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+// y in boxes of 32 rows x 128 bytes
+cudaError_t out_map(void* map, const void* base, uint64_t cols, uint64_t rows, uint64_t stride, bool bf16) {
+    return encode_map(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, cols, rows, stride,
+                      bf16 ? 64 : 32, 32);
+}
+}  // namespace
+
+cudaError_t byte_map(void* map, const void* base, uint64_t cols, uint64_t rows, uint64_t stride, int box_rows) {
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, cols, rows, stride, kBlk, box_rows);
 }
 
 int sm_count() {
@@ -68,15 +80,16 @@ constexpr int kTileBytes = kBlk * kBlk;  // one 128 x 128 operand tile: 16 KB
 
 // ------------------------------------------------------------------- many rows
 
-constexpr int kBufs = 2;                 // TMEM buffers
+constexpr int kTmemCols = 512;            // two or four buffers of a tile's width
+constexpr int kMaxBufs = 4;
 constexpr int kTInfo = 4;                // tiles published ahead
+constexpr int kIssuers = 2;
 constexpr int kPromoWarps = 8;
 constexpr int kThreads = 128 + 32 * kPromoWarps;
-// Register split (setmaxnreg): 168 a thread at launch; warpgroup 0 drops to 32, the promotion rises to 232.
-constexpr int kRegsLow = 32, kRegsHigh = 232;
+// Register split (setmaxnreg): 168 a thread at launch; warpgroup 0 drops to 40, the promotion rises to 232.
+constexpr int kRegsLow = 40, kRegsHigh = 232;
 static_assert(128 * kRegsLow + 32 * kPromoWarps * kRegsHigh <= kThreads * 168, "register split");
-constexpr int kStageRow = 80;            // bytes of an output row in the staging buffer: 64 + 16 against bank conflicts
-constexpr int kStageBytes = 32 * kStageRow;
+constexpr int kOutBytes = 8192;          // staging of a promotion warp: 32 rows x 128 bytes, once or twice
 
 struct TileInfo {
     int end;
@@ -86,17 +99,13 @@ struct TileInfo {
     int64_t row0;
 };
 
-template <int H>
-constexpr int stages() {
-    return H == 2 ? 4 : 5;
-}
+constexpr int kStages = 4;
 
-template <int H>
 struct Smem {
-    alignas(1024) uint8_t ring[stages<H>()][(1 + H) * kTileBytes];
-    uint8_t out[kPromoWarps][kStageBytes];
-    uint64_t full[stages<H>()], empty[stages<H>()];
-    uint64_t accf[kBufs], acce[kBufs];
+    alignas(1024) uint8_t ring[kStages][2 * kTileBytes];  // 128 activation rows, 128 weight rows
+    alignas(1024) uint8_t out[kPromoWarps][kOutBytes];
+    uint64_t full[kStages], empty[kStages];
+    uint64_t accf[kMaxBufs], acce[kMaxBufs];
     uint64_t tfull[kTInfo], tempty[kTInfo];
     TileInfo ti[kTInfo];
     uint32_t tmem;
@@ -107,8 +116,8 @@ struct Smem {
 
 // Offsets of the groups, made harmless: within [0, M] and not decreasing, whatever the array holds.
 // Warp 0 of the CTA; 32 groups a step.
-template <int H>
-__device__ __forceinline__ void load_groups(const Product& p, Smem<H>* sm, int lane) {
+template <int kRows>
+__device__ __forceinline__ void load_groups(const Product& p, Smem* sm, int lane) {
     int prev = 0, base = 0;
     for (int g0 = 0; g0 < p.groups; g0 += 32) {
         const int g = g0 + lane;
@@ -130,7 +139,7 @@ __device__ __forceinline__ void load_groups(const Product& p, Smem<H>* sm, int l
         }
         int before = __shfl_up_sync(0xffffffffu, o, 1);
         if (lane == 0) before = prev;
-        int t = g < p.groups ? (o - before + kBlk - 1) / kBlk : 0;
+        int t = g < p.groups ? (o - before + kRows - 1) / kRows : 0;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int u = __shfl_up_sync(0xffffffffu, t, d);
@@ -146,53 +155,50 @@ __device__ __forceinline__ void load_groups(const Product& p, Smem<H>* sm, int l
     __syncwarp();
 }
 
-// 64 bytes of an output row: a staging row, written by the thread that owns the row ...
-__device__ __forceinline__ void stage_row(uint8_t* row, const float2* acc, __nv_bfloat16) {
+// A box of the staging buffer: 32 rows of 128 bytes, 16-byte chunk c of row r at chunk c ^ (r & 7) (the 128-byte
+// swizzle of the copy engine, and no bank conflict).  The thread that owns row r writes it from its accumulators ...
+__device__ __forceinline__ void stage_row(uint8_t* box, int r, const float2* acc, __nv_bfloat16) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4*>(row + 16 * i) =
+    for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4*>(box + r * 128 + ((i ^ (r & 7)) << 4)) =
             make_uint4(bf16x2(acc[4 * i].x, acc[4 * i].y), bf16x2(acc[4 * i + 1].x, acc[4 * i + 1].y),
                        bf16x2(acc[4 * i + 2].x, acc[4 * i + 2].y), bf16x2(acc[4 * i + 3].x, acc[4 * i + 3].y));
 }
-__device__ __forceinline__ void stage_row(uint8_t* row, const float2* acc, float) {
+__device__ __forceinline__ void stage_row(uint8_t* box, int r, const float2* acc, float) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4*>(row + 16 * i) = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+    for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<float4*>(box + r * 128 + ((i ^ (r & 7)) << 4)) =
+            make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
 }
 
-// ... and the warp's 32 such rows on to global memory, 4 lanes a row (16 bytes each) where the row of y
-// and the columns allow it, else element by element.
+// ... and where the copy engine may not write it (rows behind the tile's that belong to another group, rows of y that
+// are not whole 16 bytes) the warp does, element by element.
 template <class T>
-__device__ __forceinline__ void store_rows(const uint8_t* st, T* y, int64_t ldy, int nr, int col, int N, bool wide,
-                                           int lane) {
-    constexpr int kCols = 64 / (int)sizeof(T);
-    if (col >= N) return;
-    if (wide && col + kCols <= N) {
-        const int c = lane & 3;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = i * 8 + (lane >> 2);
-            if (r < nr)
-                *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(y + r * ldy + col) + 16 * c) =
-                    *reinterpret_cast<const uint4*>(st + r * kStageRow + 16 * c);
-        }
-        return;
+__device__ __forceinline__ void store_box(const uint8_t* box, T* y, int64_t ldy, int nr, int col, int N, int lane) {
+    constexpr int kCols = 128 / (int)sizeof(T);
+    for (int c = lane; c < kCols; c += 32) {
+        if (col + c >= N) break;
+        const int byte = c * (int)sizeof(T);
+        for (int r = 0; r < nr; ++r)
+            y[r * ldy + col + c] = *reinterpret_cast<const T*>(box + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15));
     }
-    const int c = lane % kCols;
-    for (int r = lane / kCols; r < nr; r += 32 / kCols)
-        if (col + c < N) y[r * ldy + col + c] = *reinterpret_cast<const T*>(st + r * kStageRow + c * (int)sizeof(T));
 }
 
-template <int H, class T>
+template <bool kPair, class T>
 __global__ void __launch_bounds__(kThreads, 1)
-product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap, const Product p)
+product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
+               const __grid_constant__ CUtensorMap ymap, const bool wide, const Product p)
 {
-    constexpr int S = stages<H>();
-    constexpr int kTx = (1 + H) * kTileBytes;
-    constexpr int kCols = 64;  // columns of each half a promotion thread owns
+    constexpr int C = kPair ? 2 : 1;          // CTAs a tile
+    constexpr int kRows = C * kBlk;           // its rows
+    constexpr int H = C;                      // its columns: H halves of 128
+    constexpr int kBuf = H * kBlk, kBufs = kTmemCols / kBuf;  // a block's product, and how many of them TMEM holds
+    constexpr int S = kStages;
+    constexpr int kCols = kPair ? 128 : 64;   // columns that a promotion thread owns: a half, or half of the only one
     extern __shared__ uint8_t smem_raw[];
-    Smem<H>* sm = reinterpret_cast<Smem<H>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Smem* sm = reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = kPair ? (int)cluster_rank() : 0;
     const int KB = (p.K + kBlk - 1) / kBlk, nb = (p.N + kBlk - 1) / kBlk, ntiles = (nb + H - 1) / H;
 
     if (tid == 0) {
@@ -202,22 +208,27 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
         }
         for (int i = 0; i < kBufs; ++i) {
             mbar_init(&sm->accf[i], 1);
-            mbar_init(&sm->acce[i], kPromoWarps);
+            mbar_init(&sm->acce[i], C * kPromoWarps);
         }
         for (int i = 0; i < kTInfo; ++i) {
             mbar_init(&sm->tfull[i], 1);
-            mbar_init(&sm->tempty[i], 1 + kPromoWarps);
+            mbar_init(&sm->tempty[i], kIssuers + kPromoWarps);
         }
         sm->abort = 0;
         async::fence_barrier_init();
     }
     if (warp == 1) {
-        tc5::tmem_alloc(&sm->tmem, kBufs * H * kBlk);
+        if (kPair) tmem_alloc_pair(&sm->tmem, kTmemCols);
+        else tc5::tmem_alloc(&sm->tmem, kTmemCols);
         tc5::before_sync();
     }
-    dep_wait();
     __syncthreads();
+    if (kPair) {  // the barriers of both CTAs exist before either is signalled
+        cluster_arrive();
+        cluster_wait();
+    }
     tc5::after_sync();
+    dep_wait();
     dep_launch();  // not before this CTA has its TMEM: a dependent that waits for this grid may take the rest
     const uint32_t tmem = sm->tmem;
 
@@ -226,14 +237,14 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
         if (warp == 0) {
             int64_t total;
             if (p.groups) {
-                load_groups<H>(p, sm, lane);
+                load_groups<kRows>(p, sm, lane);
                 total = (int64_t)sm->tiles[p.groups] * ntiles;
             } else {
-                total = (p.M + kBlk - 1) / kBlk * ntiles;
+                total = (p.M + kRows - 1) / kRows * ntiles;
             }
             int sc = 0, tc = 0;
             bool ok = true;
-            for (int64_t L = blockIdx.x; ok; L += gridDim.x, ++tc) {
+            for (int64_t L = blockIdx.x / C; ok; L += gridDim.x / C, ++tc) {
                 const int b = tc % kTInfo;
                 if (tc >= kTInfo && !warp_wait(&sm->tempty[b], (tc / kTInfo - 1) & 1, &sm->abort, p.err, 1)) break;
                 TileInfo& ti = sm->ti[b];
@@ -248,7 +259,7 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                 const int64_t mt = L / ntiles;
                 const int nt = (int)(L - mt * ntiles);
                 int g = 0;
-                int64_t row0 = mt * kBlk, rows = p.M;
+                int64_t row0 = mt * kRows, rows = p.M;
                 if (p.groups) {
                     int lo = 0, hi = p.groups - 1;  // the last group with tiles[g] <= mt
                     while (lo < hi) {
@@ -257,19 +268,24 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                         else hi = mid - 1;
                     }
                     g = lo;
-                    row0 = sm->off[g] + (mt - sm->tiles[g]) * kBlk;
+                    row0 = sm->off[g] + (mt - sm->tiles[g]) * kRows;
                     rows = sm->off[g + 1];
                 }
                 const int n0 = nt * H * kBlk;
+                // CTA 1 of a pair may have no rows: then it loads none, and its half of the product is not used
+                const bool second = row0 + kBlk < rows;
+                row0 += rank * kBlk;
+                const int nr = (int)min((int64_t)kBlk, max(rows - row0, (int64_t)0));
                 if (lane == 0) {
                     ti.end = 0;
-                    ti.nr = (int)min((int64_t)kBlk, rows - row0);
+                    ti.nr = nr;
                     ti.n0 = n0;
                     ti.sw0 = (g * nb + nt * H) * KB;
                     ti.row0 = row0;
                     mbar_arrive(&sm->tfull[b]);
                 }
-                const int w0 = g * p.N + n0;
+                const int w0 = g * p.N + n0 + rank * kBlk;
+                const uint32_t tx = kPair ? (second ? 4 : 3) * kTileBytes : 2 * kTileBytes;
                 for (int kb = 0; kb < KB; ++kb, ++sc) {
                     const int s = sc % S;
                     if (sc >= S && !warp_wait(&sm->empty[s], (sc / S - 1) & 1, &sm->abort, p.err, 2)) {
@@ -277,22 +293,31 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                         break;
                     }
                     if (elect()) {
-                        mbar_expect_tx(&sm->full[s], kTx);
-                        tc5::tma_load_2d(sm->ring[s], &amap, kb * kBlk, (int)row0, &sm->full[s]);
-#pragma unroll
-                        for (int h = 0; h < H; ++h)
-                            tc5::tma_load_2d(sm->ring[s] + (1 + h) * kTileBytes, &wmap, kb * kBlk, w0 + h * kBlk,
-                                             &sm->full[s]);
+                        if (kPair) {
+                            const uint32_t bar = peer_addr(&sm->full[s], 0);
+                            if (rank == 0) mbar_expect_tx(&sm->full[s], tx);
+                            if (nr > 0) tma_load_2d_pair(sm->ring[s], &amap, kb * kBlk, (int)row0, bar);
+                            tma_load_2d_pair(sm->ring[s] + kTileBytes, &wmap, kb * kBlk, w0, bar);
+                        } else {
+                            mbar_expect_tx(&sm->full[s], tx);
+                            tc5::tma_load_2d(sm->ring[s], &amap, kb * kBlk, (int)row0, &sm->full[s]);
+                            tc5::tma_load_2d(sm->ring[s] + kTileBytes, &wmap, kb * kBlk, w0, &sm->full[s]);
+                        }
                     }
                     __syncwarp();
                 }
             }
-            // every copy has landed before the CTA may exit
-            for (int i = max(sc - S, 0); i < sc; ++i) wait_drain(&sm->full[i % S], (i / S) & 1);
-        } else if (warp == 1) {
-            // the warp walks together and one lane issues: in a branch of one lane the same loop starves beside the
-            // promotion warps
-            int sc = 0, tc = 0;
+            // every copy has landed before the CTA may exit; CTA 0's barriers count those of both
+            if (rank == 0)
+                for (int i = max(sc - S, 0); i < sc; ++i) wait_drain(&sm->full[i % S], (i / S) & 1);
+        } else if (warp <= kIssuers) {
+            // Two warps issue in turn, a block of K each: its MMAs run for 515 clocks, but what one warp does for it
+            // (three waits, eight MMAs, three commits) takes longer.  A warp walks together and one lane issues: in a
+            // branch of one lane the same loop takes half as long again.  Each warp keeps to its own buffers and ring
+            // stages, so that no phase of a barrier passes unseen.
+            static_assert(kIssuers == 2 && kStages % 2 == 0 && kBufs % 2 == 0, "ownership");
+            const uint64_t ring_desc = tc5::smem_desc_sw128(sm->ring[0]);
+            int sc = 0, mine = warp - 1, tc = 0, last = -1;  // blocks of K so far, this warp's next; its last buffer
             bool ok = true;
             while (ok) {
                 const int b = tc % kTInfo;
@@ -302,113 +327,159 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                 if (lane == 0) mbar_arrive(&sm->tempty[b]);
                 ++tc;
                 if (end) break;
-                for (int kb = 0; kb < KB; ++kb, ++sc) {
-                    const int s = sc % S, d = sc % kBufs;
-                    if (!warp_wait(&sm->full[s], (sc / S) & 1, &sm->abort, p.err, 4) ||
-                        !warp_wait(&sm->acce[d], (sc / kBufs) & 1, &sm->abort, p.err, 5)) {
-                        ok = false;
-                        break;
-                    }
+                if (rank != 0) continue;  // CTA 0 issues for both
+                sc += KB;
+                for (; mine < sc && ok; mine += kIssuers) {
+                    const int s = mine % S, d = mine % kBufs;
+                    ok = warp_wait2(&sm->full[s], (mine / S) & 1, &sm->acce[d], (mine / kBufs) & 1, &sm->abort, p.err, 4);
+                    if (!ok) break;
                     tc5::after_sync();
-                    const uint64_t ad = tc5::smem_desc_sw128(sm->ring[s]);
-                    const uint64_t wd = tc5::smem_desc_sw128(sm->ring[s] + kTileBytes);
-                    const uint32_t dt = tmem + d * H * kBlk;
+                    const uint64_t ad = ring_desc + (uint64_t)(s * (2 * kTileBytes >> 4)), wd = ad + (kTileBytes >> 4);
+                    const uint32_t dt = tmem + d * kBuf;
                     if (elect()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)  // 32 of K (32 bytes, 2 descriptor units) each
-                            mma_e4m3(dt, ad + 2 * k, wd + 2 * k, idesc_e4m3(H * kBlk), k > 0);
-                        tc5::commit(&sm->empty[s]);
-                        tc5::commit(&sm->accf[d]);
+                        for (int k = 0; k < 4; ++k) {  // 32 of K (32 bytes, 2 descriptor units) each
+                            if (kPair) mma_e4m3_pair(dt, ad + 2 * k, wd + 2 * k, idesc_e4m3_pair(kBuf), k > 0);
+                            else mma_e4m3(dt, ad + 2 * k, wd + 2 * k, idesc_e4m3(kBuf), k > 0);
+                        }
+                        if (kPair) {
+                            commit_pair(&sm->accf[d]);
+                            commit_pair(&sm->empty[s]);
+                        } else {
+                            tc5::commit(&sm->accf[d]);
+                            tc5::commit(&sm->empty[s]);
+                        }
                     }
                     __syncwarp();
+                    last = mine;
                 }
             }
             // every MMA has completed before TMEM is released
-            if (sc > 0) wait_drain(&sm->accf[(sc - 1) % kBufs], ((sc - 1) / kBufs) & 1);
+            if (last >= 0) wait_drain(&sm->accf[last % kBufs], (last / kBufs) & 1);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
-        const int quarter = warp & 3, cg = (warp - 4) >> 2;
+        // a pair's warps 4..7 take the first half of the columns and 8..11 the second; of a single CTA's tile they take
+        // 64 columns each
+        const int quarter = warp & 3, set = (warp - 4) >> 2, half = kPair ? set : 0;
         const int row = quarter * 32 + lane;
-        const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + cg * kCols;
-        uint8_t* stage = sm->out[warp - 4];
-        const bool wide = ((reinterpret_cast<uintptr_t>(p.y) | (uintptr_t)(p.ldy * (int)sizeof(T))) & 15) == 0;
+        const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + set * kCols;
+        const uint32_t acce = peer_addr(&sm->acce[0], 0);  // of the CTA that issues
+        uint8_t* out = sm->out[warp - 4];
         if (lane == 0)
-            for (int b = 0; b < kBufs; ++b) mbar_arrive(&sm->acce[b]);
-        int sc = 0, tc = 0;
-        bool ok = true;
-        while (ok) {
+            for (int b = 0; b < kBufs; ++b) peer_arrive_read(acce + b * 8);
+        int n = 0, tc = 0;
+        // the next tile, and its first two blocks' scales on their way
+        TileInfo ti;
+        const float *sa, *sw;
+        float a[2], w[2];
+        const auto scales = [&](int i, int kb) {
+            a[i] = sa[kb];
+            w[i] = sw[kb];
+        };
+        const auto next = [&]() -> bool {
             const int tb = tc % kTInfo;
-            if (!warp_wait(&sm->tfull[tb], (tc / kTInfo) & 1, &sm->abort, p.err, 6)) break;
-            const TileInfo ti = sm->ti[tb];
+            if (!warp_wait(&sm->tfull[tb], (tc / kTInfo) & 1, &sm->abort, p.err, 6)) return false;
+            ti = sm->ti[tb];
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->tempty[tb]);
             ++tc;
-            if (ti.end) break;
-            const float* sa = p.sa + (ti.row0 + min(row, ti.nr - 1)) * KB;
-            const float* sw = p.sw + ti.sw0;
-            const int second = (H == 2 && ti.n0 + kBlk < p.N) ? KB : 0;  // a last half past the matrix: unused columns
-            float2 acc[H][kCols / 2];
+            if (ti.end) return false;
+            sa = p.sa + min(ti.row0 + row, p.M - 1) * KB;  // rows past the tile's: not used
+            // a half past the matrix (its columns are not used) takes the first one's scales
+            sw = p.sw + ti.sw0 + (ti.n0 + half * kBlk < p.N ? half * KB : 0);
+            scales(0, 0);
+            scales(1, KB > 1 ? 1 : 0);
+            return true;
+        };
+        bool more = next();
+        while (more) {
+            float2 acc[kCols / 2];
 #pragma unroll
-            for (int h = 0; h < H; ++h)
-#pragma unroll
-                for (int c = 0; c < kCols / 2; ++c) acc[h][c] = make_float2(0.0f, 0.0f);
-            float a1 = sa[0], w0 = sw[0], w1 = sw[second];
-            for (int kb = 0; kb < KB; ++kb, ++sc) {
-                const int d = sc % kBufs;
-                const float s[2] = {a1 * w0, a1 * w1};
-                if (kb + 1 < KB) {
-                    a1 = sa[kb + 1];
-                    w0 = sw[kb + 1];
-                    w1 = sw[second + kb + 1];
-                }
-                if (!warp_wait(&sm->accf[d], (sc / kBufs) & 1, &sm->abort, p.err, 7)) {
-                    ok = false;
-                    break;
-                }
+            for (int c = 0; c < kCols / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
+            uint32_t v[2][32];
+            bool ok = warp_wait(&sm->accf[n % kBufs], (n / kBufs) & 1, &sm->abort, p.err, 7);
+            if (ok) {
                 tc5::after_sync();
-                const uint32_t ta = tl + d * H * kBlk;
-                // 32 columns at a time, each load under the additions of the one before; the buffer goes
-                // back to the MMA when the last has landed
-                uint32_t v[2][32];
-                tc5::tmem_ld32(ta, v[0]);
+                tc5::tmem_ld32(tl + n % kBufs * kBuf, v[0]);
+            }
+            for (int kb = 0; kb < KB && ok; ++kb) {
+                const float s = a[0] * w[0];
+                a[0] = a[1];
+                w[0] = w[1];
+                if (kb + 2 < KB) scales(1, kb + 2);
+                const int d = n % kBufs;
+                ++n;
+                uint64_t* const after = &sm->accf[n % kBufs];
+                // 32 columns at a time, each load under the additions of the one before; a buffer goes back to the MMA
+                // when its last load has landed
 #pragma unroll
-                for (int i = 0; i < 2 * H; ++i) {
+                for (int i = 0; i < kCols / 32; ++i) {
                     tc5::tmem_wait_ld(v[i & 1]);
-                    if (i + 1 < 2 * H) {
-                        tc5::tmem_ld32(ta + ((i + 1) >> 1) * kBlk + ((i + 1) & 1) * 32, v[(i + 1) & 1]);
+                    if (i + 1 < kCols / 32) {
+                        tc5::tmem_ld32(tl + d * kBuf + (i + 1) * 32, v[(i + 1) & 1]);
                     } else {
                         tc5::before_sync();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm->acce[d]);
+                        if (lane == 0) peer_arrive_read(acce + d * 8);
                     }
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        float2& to = acc[i >> 1][(i & 1) * 16 + c];
-                        to.x = fmaf(__uint_as_float(v[i & 1][2 * c]), s[i >> 1], to.x);
-                        to.y = fmaf(__uint_as_float(v[i & 1][2 * c + 1]), s[i >> 1], to.y);
+                        float2& to = acc[i * 16 + c];
+                        to.x = fmaf(__uint_as_float(v[i & 1][2 * c]), s, to.x);
+                        to.y = fmaf(__uint_as_float(v[i & 1][2 * c + 1]), s, to.y);
+                    }
+                }
+                if (kb + 1 < KB) {
+                    ok = warp_wait(after, (n / kBufs) & 1, &sm->abort, p.err, 8);
+                    if (ok) {
+                        tc5::after_sync();
+                        tc5::tmem_ld32(tl + n % kBufs * kBuf, v[0]);
                     }
                 }
             }
-            if (!ok || *reinterpret_cast<volatile int*>(&sm->abort)) break;
-            constexpr int kChunk = 64 / (int)sizeof(T);
-            T* y = static_cast<T*>(p.y) + (ti.row0 + quarter * 32) * p.ldy;
-            const int nr = min(ti.nr - quarter * 32, 32);
+            if (!ok || __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&sm->abort))) break;
+            constexpr int kBox = 128 / (int)sizeof(T);           // columns of a box
+            constexpr int kRound = kOutBytes / (32 * 128);       // boxes staged at once
+            const int64_t y0 = ti.row0 + quarter * 32;
+            const int nr = min(ti.nr - quarter * 32, 32), n0 = ti.n0 + half * kBlk + (kPair ? 0 : set * kCols);
+            more = next();
+            if (nr <= 0) continue;
+            // a box whose rows are all the tile's, or behind the matrix, is left to the copy engine
+            const bool engine = wide && (nr == 32 || y0 + nr == p.M);
 #pragma unroll
-            for (int h = 0; h < H; ++h)
+            for (int b0 = 0; b0 < kCols / kBox; b0 += kRound) {
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
 #pragma unroll
-                for (int c = 0; c < kCols / kChunk; ++c) {
-                    stage_row(stage + lane * kStageRow, &acc[h][c * kChunk / 2], T());
-                    __syncwarp();
-                    store_rows<T>(stage, y, p.ldy, nr, ti.n0 + h * kBlk + cg * kCols + c * kChunk, p.N, wide, lane);
-                    __syncwarp();
+                for (int b = b0; b < b0 + kRound && b < kCols / kBox; ++b)
+                    stage_row(out + (b - b0) * 32 * 128, lane, &acc[b * kBox / 2], T());
+                fence_async_smem();
+                __syncwarp();
+#pragma unroll
+                for (int b = b0; b < b0 + kRound && b < kCols / kBox; ++b) {
+                    const int col = n0 + b * kBox;
+                    if (!engine) store_box<T>(out + (b - b0) * 32 * 128, static_cast<T*>(p.y) + y0 * p.ldy, p.ldy, nr, col, p.N, lane);
+                    else if (lane == 0 && col < p.N) tma_store_2d(&ymap, out + (b - b0) * 32 * 128, col, (int)y0);
                 }
+                if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                __syncwarp();
+            }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the writes are done, not only read
+        __syncwarp();
     }
     tc5::before_sync();
     __syncthreads();
+    if (kPair) {  // neither CTA leaves while the other may signal its barriers or the pair's MMAs read its operands
+        cluster_arrive();
+        cluster_wait();
+    }
     tc5::after_sync();
-    if (warp == 1) tc5::tmem_dealloc(tmem, kBufs * H * kBlk);
+    if (warp == 1) {
+        if (kPair) tmem_dealloc_pair(tmem, kTmemCols);
+        else tc5::tmem_dealloc(tmem, kTmemCols);
+    }
 }
 
 // -------------------------------------------------------------------- few rows
@@ -517,27 +588,46 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
             // operand rows of this round: a half warp per (row, block)
             const int n = min(kRound, mine - i0);
             const int hl = pt & 15;
-            for (int j = pt >> 4; j < n * m; j += 8) {
-                const int r = j / m, t = j - r * m;
-                const int kb = rank + (i0 + r) * C, col = kb * kBlk + hl * 8;
-                uint2 code = make_uint2(0u, 0u);
-                if (p.x) {
-                    float v[8] = {};
-                    if (col < p.K) load8(p.x + t * p.ldx + col, v);
-                    // the half warps of a warp may part at the end of the loop
-                    uint32_t am = amax8(v);
+            constexpr int kBatch = NT / 8;  // in flight a half warp: every row of a block
+            const float inv = __fdividef(1.0f, (float)m);
+            // (both half warps of a warp make the same turns: they meet in the shuffles)
+            for (int jw = pt >> 5 << 1; jw < n * m; jw += 8 * kBatch) {
+                const int j0 = jw + (pt >> 4 & 1);
+                uint4 raw[kBatch] = {};
+                float sc[kBatch];
+                int at[kBatch];
 #pragma unroll
-                    for (int o = 8; o > 0; o >>= 1)
-                        am = max(am, __shfl_xor_sync(0xffffu << (threadIdx.x & 16), am, o));
-                    const float sc = scale_of(am);
-                    code = make_uint2(e4m3x4(v, sc), e4m3x4(v + 4, sc));
-                    if (hl == 0) sm->sx[r][t] = sc;
-                } else {
-                    if (col < p.K) code = *reinterpret_cast<const uint2*>(p.a + (int64_t)t * p.K + col);
-                    if (hl == 0) sm->sx[r][t] = p.sa[(int64_t)t * KB + kb];
+                for (int u = 0; u < kBatch; ++u) {
+                    if (jw + 8 * u >= n * m) continue;
+                    const int j = min(j0 + 8 * u, n * m - 1);            // the last one may be read by both
+                    const int r = (int)(((float)j + 0.5f) * inv), t = j - r * m;  // exact: j is below 2^12
+                    const int kb = rank + (i0 + r) * C, col = kb * kBlk + hl * 8;
+                    at[u] = r * NT + t;
+                    if (p.x) {
+                        if (col < p.K) raw[u] = *reinterpret_cast<const uint4*>(p.x + t * p.ldx + col);
+                    } else {
+                        if (col < p.K) {
+                            const uint2 q = *reinterpret_cast<const uint2*>(p.a + (int64_t)t * p.K + col);
+                            raw[u].x = q.x;
+                            raw[u].y = q.y;
+                        }
+                        sc[u] = p.sa[(int64_t)t * KB + kb];
+                    }
                 }
-                // 128-byte swizzle: 16-byte chunk c of row t lies at chunk c ^ (t & 7)
-                *reinterpret_cast<uint2*>(sm->b + (r * NT + t) * kBlk + (((hl >> 1) ^ (t & 7)) << 4) + (hl & 1) * 8) = code;
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    if (jw + 8 * u >= n * m) continue;
+                    uint2 code = make_uint2(raw[u].x, raw[u].y);
+                    if (p.x) {
+                        float v[8];
+                        unpack8(raw[u], v);
+                        sc[u] = scale_of(half_warp_max(amax8(v)));
+                        code = Coder(sc[u])(v);
+                    }
+                    if (hl == 0) (&sm->sx[0][0])[at[u]] = sc[u];
+                    // 128-byte swizzle: 16-byte chunk c of row t lies at chunk c ^ (t & 7) (NT is a multiple of 8)
+                    *reinterpret_cast<uint2*>(sm->b + at[u] * kBlk + (((hl >> 1) ^ (at[u] & 7)) << 4) + (hl & 1) * 8) = code;
+                }
             }
             fence_async_smem();
             mbar_arrive(&sm->ready);
@@ -639,12 +729,21 @@ cudaError_t launch(K kern, unsigned grid, unsigned threads, size_t smem, int clu
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int H>
+template <bool kPair>
 cudaError_t launch_many(const Product& p, const CUtensorMap& am, const CUtensorMap& wm, int64_t tiles, cudaStream_t st) {
-    const unsigned grid = (unsigned)std::min<int64_t>(tiles, sm_count());
-    const size_t smem = sizeof(Smem<H>) + 1024;
-    return p.y_bf16 ? launch(product_kernel<H, __nv_bfloat16>, grid, kThreads, smem, 1, st, am, wm, p)
-                    : launch(product_kernel<H, float>, grid, kThreads, smem, 1, st, am, wm, p);
+    // y for the copy engine, where it is laid out for it: it writes whole 16 bytes, past the last column too
+    const int64_t es = p.y_bf16 ? 2 : 4;
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.y) | (uintptr_t)(p.ldy * es) | (uintptr_t)(p.N * es)) & 15) == 0;
+    CUtensorMap ym = {};
+    if (wide) {
+        const cudaError_t e = out_map(&ym, p.y, (uint64_t)p.N, (uint64_t)p.M, (uint64_t)(p.ldy * es), p.y_bf16);
+        if (e != cudaSuccess) return e;
+    }
+    constexpr int C = kPair ? 2 : 1;
+    const unsigned grid = (unsigned)std::min<int64_t>(tiles, sm_count() / C) * C;
+    const size_t smem = sizeof(Smem) + 1024;
+    return p.y_bf16 ? launch(product_kernel<kPair, __nv_bfloat16>, grid, kThreads, smem, C, st, am, wm, ym, wide, p)
+                    : launch(product_kernel<kPair, float>, grid, kThreads, smem, C, st, am, wm, ym, wide, p);
 }
 
 template <int NT>
@@ -661,14 +760,18 @@ cudaError_t launch_product(const Product& p, cudaStream_t st) {
     CUtensorMap am, wm;
     const int64_t G = p.groups ? p.groups : 1;
     cudaError_t e = byte_map(&am, p.a, (uint64_t)p.K, (uint64_t)p.M, (uint64_t)p.K, kBlk);
-    if (e == cudaSuccess) e = byte_map(&wm, p.w, (uint64_t)p.K, (uint64_t)(G * p.N), (uint64_t)p.K, kBlk);
     if (e != cudaSuccess) return e;
     // tiles at most: each group may end inside a tile of rows
-    const int64_t mt = p.groups ? std::min<int64_t>(p.M / kBlk + p.groups, p.M) : blocks_of(p.M);
-    const int64_t nb = blocks_of(p.N);
-    // 256 columns a tile read the activations half as often; 128 where that leaves SMs without a tile
-    if (nb > 1 && mt * ((nb + 1) / 2) >= sm_count()) return launch_many<2>(p, am, wm, mt * ((nb + 1) / 2), st);
-    return launch_many<1>(p, am, wm, mt * nb, st);
+    const auto row_tiles = [&](int64_t rows) {
+        return p.groups ? std::min<int64_t>(p.M / rows + p.groups, p.M) : (p.M + rows - 1) / rows;
+    };
+    const int64_t nb = blocks_of(p.N), pairs = row_tiles(2 * kBlk) * ((nb + 1) / 2);
+    // pairs of CTAs where there are tiles for all of them
+    const bool pair = nb > 1 && 2 * pairs >= sm_count();
+    e = byte_map(&wm, p.w, (uint64_t)p.K, (uint64_t)(G * p.N), (uint64_t)p.K, kBlk);
+    if (e != cudaSuccess) return e;
+    if (pair) return launch_many<true>(p, am, wm, pairs, st);
+    return launch_many<false>(p, am, wm, row_tiles(kBlk) * nb, st);
 }
 
 cudaError_t launch_product_small(const Product& p, cudaStream_t st) {

@@ -83,7 +83,7 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
             if (b < KB && c < p.d) load8(p.x + (int64_t)mt * p.d + c, v);
             const float s = scale_of(half_warp_max(amax8(v)));
             if (b < KB && c < p.d)
-                *reinterpret_cast<uint2*>(p.xq + (int64_t)mt * p.d + c) = make_uint2(e4m3x4(v, s), e4m3x4(v + 4, s));
+                *reinterpret_cast<uint2*>(p.xq + (int64_t)mt * p.d + c) = Coder(s)(v);
             if (b < KB && hl == 0) p.sx[mt * KB + b] = s;
         }
         if (tid < 16) p.arrived[mt * 16 + tid] = 0;
@@ -456,7 +456,7 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffu << (threadIdx.x & 16), am, o));
                 const float s = scale_of(am);
-                *reinterpret_cast<uint2*>(operand_at(operand, kb, t, hl * 8)) = make_uint2(e4m3x4(v, s), e4m3x4(v + 4, s));
+                *reinterpret_cast<uint2*>(operand_at(operand, kb, t, hl * 8)) = Coder(s)(v);
                 if (hl == 0) sh[kb * kN + t] = s;
             }
         }

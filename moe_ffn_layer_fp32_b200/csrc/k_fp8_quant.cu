@@ -21,15 +21,19 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const T* x, int
     const int hl = threadIdx.x & 15;
     dep_launch();
     dep_wait();
-    const int64_t first = ((int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4)) * kItems;
+    constexpr int kPer = kThreads / 16 * kItems;  // blocks a CTA takes, kItems in a row a half warp
+    const int64_t begin = (int64_t)blockIdx.x * kPer, row0 = begin / kb;
+    const int b0 = (int)(begin - row0 * kb), mine = (threadIdx.x >> 4) * kItems;
+    const int64_t first = begin + mine;
     float v[kItems][8];
     int64_t row[kItems];
     int col[kItems];
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
         const int64_t b = first + i;
-        row[i] = b / kb;
-        col[i] = (int)(b - row[i] * kb) * kBlk + hl * 8;
+        const int at = b0 + mine + i, down = at / kb;  // 64-bit divisions for each block took three times the copy's time
+        row[i] = row0 + down;
+        col[i] = (at - down * kb) * kBlk + hl * 8;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
         if (b < nblk && col[i] < K) load8(x + row[i] * ldx + col[i], v[i]);
@@ -40,7 +44,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const T* x, int
         if (first + i >= nblk) continue;
         if (hl == 0) s[first + i] = sc;
         if (col[i] < K)
-            *reinterpret_cast<uint2*>(q + row[i] * K + col[i]) = make_uint2(e4m3x4(v[i], sc), e4m3x4(v[i] + 4, sc));
+            *reinterpret_cast<uint2*>(q + row[i] * K + col[i]) = Coder(sc)(v[i]);
     }
 }
 
@@ -82,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(const T* w, i
         const int n = n0 + r0 + i * (kThreads / 16);
         if (n < N && col < K)
             *reinterpret_cast<uint2*>(q + (batch * N + n) * K + col) =
-                make_uint2(e4m3x4(v[i], sc), e4m3x4(v[i] + 4, sc));
+                Coder(sc)(v[i]);
     }
 }
 

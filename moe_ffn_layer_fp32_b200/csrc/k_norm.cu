@@ -9,16 +9,39 @@
 // sum before that rounding, and the codes from x' before its rounding to BF16.
 //
 // Bound by memory: a row is read once, held in registers through both norms
-// and written once.  kG threads share a row (a warp where the registers allow
-// it: no barrier), 8 features of a thread at a time (16-byte accesses), 16
-// lanes side by side on one block of 128 features.
+// and written once.  kG threads take a row, 8 features each (16-byte accesses,
+// 16 lanes side by side on one block of 128 features), and go on to other rows:
+// the weights and a gate per feature are read once a thread, and the next row
+// is on its way while this one is reduced.
+#include <algorithm>
+
 #include "fp8.cuh"
 #include "norm.cuh"
 
 namespace mmoe {
 namespace {
 
-constexpr int kThreads = 256;
+// 8 features as they lie in memory.
+template <class T>
+struct Raw;
+template <>
+struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void get(float (&v)[8]) const { f8::unpack8(u, v); }
+};
 
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -29,110 +52,114 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
                                               f8::bf16x2(v[6], v[7]));
 }
 
-// Sum over the kG threads of a row; `part` holds one word a warp and is used once.
+// 1 / sqrt(mean(v^2) + eps) of the row that kG threads hold.  `part` holds one word a warp; the next row uses another
+// one, so that one barrier is enough.
 template <int kG>
-__device__ __forceinline__ float row_sum(float v, float* part) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (kG > 32) {
-        const int warp = threadIdx.x >> 5, first = warp / (kG / 32) * (kG / 32);
-        if ((threadIdx.x & 31) == 0) part[warp] = v;
-        __syncthreads();
-        v = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kG / 32; ++i) v += part[first + i];
-    }
-    return v;
-}
-
-// kG threads a row, kV vectors of 8 features a thread.
-template <int kG, int kV, class R, class Y>
-__global__ void __launch_bounds__(kThreads) block_norm_kernel(const NormPlan p)
-{
-    __shared__ float part[2][kThreads / 32];
-    const int g = threadIdx.x % kG;
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / kG) + threadIdx.x / kG;
-    const bool live = row < p.rows;
-    f8::dep_launch();
-    f8::dep_wait();
-    float r[kV][8], z[kV][8];
-    const bool block = p.y != nullptr;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        const int c = (i * kG + g) * 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] = z[i][j] = 0.0f;
-        if (live && c < p.d) {
-            if (block) f8::load8(static_cast<const Y*>(p.y) + row * p.ldy + c, z[i]);
-            f8::load8(static_cast<const R*>(p.r) + row * p.ldr + c, r[i]);
-        }
-    }
-    float s = 1.0f;
-    if (p.w_post) {  // the same for every thread of the grid
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kV; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(z[i][j], z[i][j], sum);
-        s = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(row_sum<kG>(sum, part[0]), (float)p.d) + p.eps));
-    }
-    const float g0 = (p.gate && p.gate_col == 0 && live) ? p.gate[row * p.gate_row] : 1.0f;
+__device__ __forceinline__ float inv_rms(const float (&v)[8], float* part, int d, float eps) {
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        const int c = (i * kG + g) * 8;
-        if (!(live && c < p.d)) continue;
-        float w[8];
-        if (p.w_post) {
-            f8::load8(p.w_post + c, w);
+    for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) z[i][j] = z[i][j] * s * w[j];
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (kG > 32) {
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+        __syncthreads();
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kG / 32; ++i) sum += part[i];
+    }
+    return __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(sum, (float)d) + eps));
+}
+
+// kG threads a row; a CTA has one row, or eight of a warp each.
+template <int kG>
+constexpr int threads() {
+    return kG == 32 ? 256 : kG;
+}
+
+// CTAs an SM: 768 threads of 80 registers, or 1024 of 64 where a row takes more.
+template <int kG>
+constexpr int resident() {
+    return (kG <= 256 ? 768 : 1024) / threads<kG>();
+}
+
+template <int kG, class R, class Y>
+__global__ void __launch_bounds__(threads<kG>(), resident<kG>()) block_norm_kernel(const NormPlan p)
+{
+    constexpr int kRows = threads<kG>() / kG;
+    __shared__ float part[2][2][kG / 32];
+    const int g = threadIdx.x % kG, c = g * 8;
+    const bool mine = c < p.d;
+    f8::dep_launch();
+    f8::dep_wait();
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kG;
+    const bool block = p.y != nullptr, per_row = p.gate && p.gate_col == 0, whole = p.gate && p.gate_col && p.gate_row;
+    Raw<R> rr = {};
+    Raw<Y> yy = {};
+    Raw<float> post = {}, pre = {}, gate = {};
+    float g0 = 1.0f;
+    const auto fetch = [&](int64_t at) {
+        if (mine) {
+            rr.load(static_cast<const R*>(p.r) + at * p.ldr + c);
+            if (block) yy.load(static_cast<const Y*>(p.y) + at * p.ldy + c);
+            if (whole) gate.load(p.gate + at * p.gate_row + c);
         }
-        if (p.gate && p.gate_col) {
-            f8::load8(p.gate + row * p.gate_row + c, w);
+        if (per_row) g0 = p.gate[at * p.gate_row];
+    };
+    if (row < p.rows) fetch(row);
+    if (mine) {
+        if (p.gate && p.gate_col && !whole) gate.load(p.gate + c);
+        if (p.w_post) post.load(p.w_post + c);
+        if (p.w_pre) pre.load(p.w_pre + c);
+    }
+    const int kb = (p.d + f8::kBlk - 1) / f8::kBlk;
+    for (int turn = 0; row < p.rows; row += step, turn ^= 1) {  // the same row for all kG threads
+        float r[8], z[8], w[8];
+        rr.get(r);
+        yy.get(z);
+        const float gr = g0;
+        float gv[8];
+        gate.get(gv);
+        if (row + step < p.rows) fetch(row + step);
+        if (p.w_post) {
+            const float s = inv_rms<kG>(z, part[turn][0], p.d, p.eps);
+            post.get(w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) z[i][j] *= w[j];
+            for (int j = 0; j < 8; ++j) z[j] = z[j] * s * w[j];
+        }
+        if (per_row) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[j] *= gr;
         } else if (p.gate) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) z[i][j] *= g0;
+            for (int j = 0; j < 8; ++j) z[j] *= gv[j];
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            r[i][j] = block ? fmaf(p.scale, r[i][j], z[i][j]) : p.scale * r[i][j];
-            sum = fmaf(r[i][j], r[i][j], sum);
-        }
-        if (p.r_out) store8(static_cast<R*>(p.r_out) + row * p.ldo + c, r[i]);
-    }
-    if (!p.w_pre) return;
-    s = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(row_sum<kG>(sum, part[1]), (float)p.d) + p.eps));
-    const int kb = (p.d + f8::kBlk - 1) / f8::kBlk;
+        for (int j = 0; j < 8; ++j) r[j] = block ? fmaf(p.scale, r[j], z[j]) : p.scale * r[j];
+        if (p.r_out && mine) store8(static_cast<R*>(p.r_out) + row * p.ldo + c, r);
+        if (!p.w_pre) continue;
+        const float s = inv_rms<kG>(r, part[turn][1], p.d, p.eps);
+        pre.get(w);
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        const int c = (i * kG + g) * 8;
-        const bool in = live && c < p.d;
-        if (in) {
-            float w[8];
-            f8::load8(p.w_pre + c, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) r[i][j] = r[i][j] * s * w[j];
-            if (p.x) store8(reinterpret_cast<__nv_bfloat16*>(p.x) + row * p.d + c, r[i]);
-        }
+        for (int j = 0; j < 8; ++j) r[j] = r[j] * s * w[j];
+        if (p.x && mine) store8(reinterpret_cast<__nv_bfloat16*>(p.x) + row * p.d + c, r);
         if (p.xq) {
-            const float sc = f8::scale_of(f8::half_warp_max(in ? f8::amax8(r[i]) : 0u));
-            if (in) {
-                *reinterpret_cast<uint2*>(p.xq + row * p.d + c) =
-                    make_uint2(f8::e4m3x4(r[i], sc), f8::e4m3x4(r[i] + 4, sc));
+            const float sc = f8::scale_of(f8::half_warp_max(mine ? f8::amax8(r) : 0u));
+            if (mine) {
+                *reinterpret_cast<uint2*>(p.xq + row * p.d + c) = f8::Coder(sc)(r);
                 if ((g & 15) == 0) p.sx[row * kb + c / f8::kBlk] = sc;
             }
         }
     }
 }
 
-template <int kG, int kV>
+template <int kG>
 cudaError_t launch(const NormPlan& p, cudaStream_t st) {
+    constexpr int kT = threads<kG>(), kRows = kT / kG;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.rows + kThreads / kG - 1) / (kThreads / kG)));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>((p.rows + kRows - 1) / kRows, (int64_t)f8::sm_count() * resident<kG>()));
+    cfg.blockDim = dim3(kT);
     cfg.stream = st;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -141,22 +168,22 @@ cudaError_t launch(const NormPlan& p, cudaStream_t st) {
     cfg.numAttrs = 1;
     using B = __nv_bfloat16;
     if (p.r_bf16)
-        return p.y_bf16 ? cudaLaunchKernelEx(&cfg, block_norm_kernel<kG, kV, B, B>, p)
-                        : cudaLaunchKernelEx(&cfg, block_norm_kernel<kG, kV, B, float>, p);
-    return p.y_bf16 ? cudaLaunchKernelEx(&cfg, block_norm_kernel<kG, kV, float, B>, p)
-                    : cudaLaunchKernelEx(&cfg, block_norm_kernel<kG, kV, float, float>, p);
+        return p.y_bf16 ? cudaLaunchKernelEx(&cfg, block_norm_kernel<kG, B, B>, p)
+                        : cudaLaunchKernelEx(&cfg, block_norm_kernel<kG, B, float>, p);
+    return p.y_bf16 ? cudaLaunchKernelEx(&cfg, block_norm_kernel<kG, float, B>, p)
+                    : cudaLaunchKernelEx(&cfg, block_norm_kernel<kG, float, float>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_block_norm(const NormPlan& p, cudaStream_t st) {
     const int v = (p.d + 7) / 8;
-    if (v <= 32) return launch<32, 1>(p, st);
-    if (v <= 64) return launch<32, 2>(p, st);
-    if (v <= 128) return launch<32, 4>(p, st);
-    if (v <= 256) return launch<64, 4>(p, st);
-    if (v <= 512) return launch<128, 4>(p, st);
-    return launch<256, 4>(p, st);
+    if (v <= 32) return launch<32>(p, st);
+    if (v <= 64) return launch<64>(p, st);
+    if (v <= 128) return launch<128>(p, st);
+    if (v <= 256) return launch<256>(p, st);
+    if (v <= 512) return launch<512>(p, st);
+    return launch<1024>(p, st);
 }
 
 }  // namespace mmoe
