@@ -168,6 +168,20 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, int
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            async::su32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(async::su32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(void* dst, const void* map, int x, int y, int z, int u, int v, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
+        "[%7];" ::"r"(async::su32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(async::su32(bar))
+        : "memory");
+}
 // A tile from shared memory to global memory (one group of the issuing thread's).
 __device__ __forceinline__ void tma_store_2d(const void* map, const void* src, int x, int y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
@@ -321,6 +335,8 @@ __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) {
 // cuTensorMap of a row-major byte matrix [rows, cols] (row stride in bytes), boxes of 128 bytes x
 // box_rows in the 128-byte swizzle layout; bytes outside the matrix read as 0.
 cudaError_t byte_map(void* map, const void* base, uint64_t cols, uint64_t rows, uint64_t stride, int box_rows);
+// The same of up to five dimensions (cols first; strides of the others in bytes), box as given.
+cudaError_t byte_map_n(void* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides, const uint32_t* box);
 int sm_count();
 
 cudaError_t launch_quantize_rows(const void* x, bool bf16, int64_t rows, int64_t K, int64_t ldx, uint8_t* q, float* s,

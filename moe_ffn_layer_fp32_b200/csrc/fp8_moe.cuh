@@ -9,6 +9,7 @@ namespace mmoe {
 namespace f8 {
 
 constexpr int kFewTokens = 64;  // largest T of the two-launch path
+constexpr int kRanks = 8;       // CTAs of a cluster, at most
 
 struct MoePlan {
     int d, h, hs, E, k, gating, T;
@@ -28,17 +29,18 @@ struct MoePlan {
     int32_t* out_idx;          // optional outputs
     float* out_gate;
     int32_t* out_counts;
+    int part_hidden, parts;    // the shared expert is taken in parts of that many hidden features
     // workspace
     int32_t* idx;              // [T, k]
     float* gate;               // [T, k]
-    uint32_t* arrived;         // [T, 16] contributions of a token that are in, per rank of a cluster
+    uint32_t* arrived;         // [T, kRanks] contributions of a token that are in, per rank of a cluster
     float* sx;                 // [T, ceil(d/128)]
     uint8_t* xq;               // [T, d]
-    float* part;               // [T, k + 1, d] expert outputs, the shared one last
+    float* part;               // [T, k, d] expert outputs, then [parts, T, d] of the shared one
     int* err;
 };
 
-// Lays the workspace out from `base`; returns its size.
+// Sets the parts of the shared expert, lays the workspace out from `base`, returns its size.
 size_t carve_moe(MoePlan& p, unsigned char* base);
 cudaError_t launch_moe_few(const MoePlan& p, cudaStream_t st);
 

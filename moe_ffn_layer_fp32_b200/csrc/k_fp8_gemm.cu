@@ -32,8 +32,8 @@ namespace mmoe {
 namespace f8 {
 
 namespace {
-cudaError_t encode_map(void* map, CUtensorMapDataType type, const void* base, uint64_t cols, uint64_t rows, uint64_t stride,
-                       int box_cols, int box_rows) {
+cudaError_t encode_map(void* map, CUtensorMapDataType type, const void* base, int rank, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box) {
     static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -43,24 +43,35 @@ cudaError_t encode_map(void* map, CUtensorMapDataType type, const void* base, ui
         return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }();
     if (!encode) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {cols, rows};
-    const cuuint64_t strides[1] = {stride};
-    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = encode(static_cast<CUtensorMap*>(map), type, 2, const_cast<void*>(base), dims, strides, box, estr,
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5], step[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        step[i] = 1;
+        if (i + 1 < rank) s[i] = strides[i];
+    }
+    const CUresult r = encode(static_cast<CUtensorMap*>(map), type, (cuuint32_t)rank, const_cast<void*>(base), d, s, b, step,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 // y in boxes of 32 rows x 128 bytes
 cudaError_t out_map(void* map, const void* base, uint64_t cols, uint64_t rows, uint64_t stride, bool bf16) {
-    return encode_map(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, cols, rows, stride,
-                      bf16 ? 64 : 32, 32);
+    const uint64_t dims[2] = {cols, rows};
+    const uint32_t box[2] = {bf16 ? 64u : 32u, 32u};
+    return encode_map(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, 2, dims, &stride, box);
 }
 }  // namespace
 
+cudaError_t byte_map_n(void* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides, const uint32_t* box) {
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rank, dims, strides, box);
+}
+
 cudaError_t byte_map(void* map, const void* base, uint64_t cols, uint64_t rows, uint64_t stride, int box_rows) {
-    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, cols, rows, stride, kBlk, box_rows);
+    const uint64_t dims[2] = {cols, rows};
+    const uint32_t box[2] = {(uint32_t)kBlk, (uint32_t)box_rows};
+    return byte_map_n(map, base, 2, dims, &stride, box);
 }
 
 int sm_count() {

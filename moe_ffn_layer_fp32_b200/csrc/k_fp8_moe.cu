@@ -12,21 +12,23 @@
 // gating, top-k; it also quantises that token's x.
 //
 // moe_experts_kernel: a cluster of S CTAs takes one expert and up to 16 of its
-// tokens (the tensor cores' smallest N).  Weights are the MMA's M: a tile is
-// 128 weight rows x 128 of K, 16 KB, one or two of them in each step of a
-// ring that runs from the first gate row to the last down row without a stop.
+// tokens (the tensor cores' smallest N).  A shared expert wider than the routed
+// ones is taken in parts of its hidden features, a cluster each, so that it is
+// not what the others wait for.  Weights are the MMA's M: a tile is up to 128
+// weight rows x 128 of K, one copy, one step of a ring that runs from the first
+// gate row to the last down row without a stop.
 //   gate/up: the CTA owns 1/S of the hidden features, over all of K.  A tile
 //     holds for each of the four TMEM lane quarters 16 gate rows and the 16 up
 //     rows of the same features, so SwiGLU needs one shuffle.
 //   exchange: once every peer has signalled its part, each CTA reads all hidden
 //     features of its tokens through distributed shared memory and quantises
-//     them for itself (a cluster barrier would also wait for the two warps that
+//     them for itself (a cluster barrier would also wait for the warps that
 //     keep the ring running).
 //   down: the CTA owns 1/S of the output rows, over all hidden features.
-// Each (token, expert) row goes to the workspace; of the k + 1 clusters that
-// a token takes part in, the last one (per rank: it owns the same output rows
-// in every cluster) adds the rows in the order of the formula.  No cluster
-// waits for another one, and no sum depends on the order of arrival.
+// Each (token, expert) row goes to the workspace; of the clusters that a token
+// takes part in, the last one (per rank: it owns the same output rows in every
+// cluster) adds the rows in the order of the formula.  No cluster waits for
+// another one, and no sum depends on the order of arrival.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -45,14 +47,15 @@ using async::mbar_expect_tx;
 using async::mbar_init;
 
 constexpr int kRouteCluster = 8;
-constexpr int kRouteThreads = 256;
+constexpr int kRouteThreads = 512;
 constexpr int kRouteParts = kRouteThreads / 64;  // K parts within a CTA
+constexpr int kRouteAhead = 16;                  // router weights a thread has in flight
 
 // ------------------------------------------------------------------ router
 
 __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteThreads) moe_route_kernel(const MoePlan p)
 {
-    extern __shared__ float route_smem[];          // x slice [8][ks]
+    extern __shared__ float route_smem[];          // x slice [ks][8]
     __shared__ float red[kRouteParts][kRouteCluster][kMaxExperts];
     __shared__ float part[kRouteCluster][kMaxExperts];
     const int tid = threadIdx.x, rank = (int)cluster_rank();
@@ -64,14 +67,22 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
     dep_launch();
     const int ks = 32 * ((p.d / 32 + kRouteCluster - 1) / kRouteCluster);
     const int k0 = min(rank * ks, p.d), n = min(ks, p.d - k0);
-    for (int i = tid; i < nt * (n / 8); i += kRouteThreads) {
-        const int t = i / (n / 8), c = (i - t * (n / 8)) * 8;
-        float v[8];
-        load8(p.x + (int64_t)(t0 + t) * p.d + k0 + c, v);
+    // thread: expert tid % 64, K part tid / 64; the first weights set out before x is read
+    const int e = tid & 63, kp = tid >> 6;
+    const float* w = p.w_router + (int64_t)k0 * p.E + e;
+    float wv[kRouteAhead];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) route_smem[t * ks + c + j] = v[j];
+    for (int i = 0; i < kRouteAhead; ++i) {
+        const int k = kp + i * kRouteParts;
+        wv[i] = e < p.E && k < n ? w[(int64_t)k * p.E] : 0.0f;
     }
-    for (int i = tid; i < (kRouteCluster - nt) * ks; i += kRouteThreads) route_smem[nt * ks + i] = 0.0f;
+    for (int i = tid; i < kRouteCluster * (n / 8); i += kRouteThreads) {
+        const int t = i & (kRouteCluster - 1), c = i / kRouteCluster * 8;
+        float v[8] = {};
+        if (t < nt) load8(p.x + (int64_t)(t0 + t) * p.d + k0 + c, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) route_smem[(c + j) * kRouteCluster + t] = v[j];
+    }
     // codes and scales of token t0 + rank, and its counters
     const int mt = t0 + rank;
     const int KB = (p.d + kBlk - 1) / kBlk;
@@ -86,19 +97,32 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
                 *reinterpret_cast<uint2*>(p.xq + (int64_t)mt * p.d + c) = Coder(s)(v);
             if (b < KB && hl == 0) p.sx[mt * KB + b] = s;
         }
-        if (tid < 16) p.arrived[mt * 16 + tid] = 0;
+        if (tid < kRanks) p.arrived[mt * kRanks + tid] = 0;
     }
     __syncthreads();
-    // thread: expert tid % 64, K part tid / 64
-    const int e = tid & 63, kp = tid >> 6;
     float acc[kRouteCluster] = {};
-    if (e < p.E) {
-        const float* w = p.w_router + (int64_t)k0 * p.E + e;
-#pragma unroll 8
-        for (int k = kp; k < n; k += kRouteParts) {
-            const float wv = w[(int64_t)k * p.E];
+    for (int i0 = 0; i0 < n; i0 += kRouteAhead * kRouteParts) {
+        float cur[kRouteAhead];
 #pragma unroll
-            for (int t = 0; t < kRouteCluster; ++t) acc[t] = fmaf(route_smem[t * ks + k], wv, acc[t]);
+        for (int i = 0; i < kRouteAhead; ++i) {
+            cur[i] = wv[i];
+            const int k = i0 + kp + (i + kRouteAhead) * kRouteParts;
+            wv[i] = e < p.E && k < n ? w[(int64_t)k * p.E] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kRouteAhead; ++i) {
+            const int k = i0 + kp + i * kRouteParts;
+            if (k >= n) break;
+            const float4 a = *reinterpret_cast<const float4*>(route_smem + k * kRouteCluster);
+            const float4 b = *reinterpret_cast<const float4*>(route_smem + k * kRouteCluster + 4);
+            acc[0] = fmaf(a.x, cur[i], acc[0]);
+            acc[1] = fmaf(a.y, cur[i], acc[1]);
+            acc[2] = fmaf(a.z, cur[i], acc[2]);
+            acc[3] = fmaf(a.w, cur[i], acc[3]);
+            acc[4] = fmaf(b.x, cur[i], acc[4]);
+            acc[5] = fmaf(b.y, cur[i], acc[5]);
+            acc[6] = fmaf(b.z, cur[i], acc[6]);
+            acc[7] = fmaf(b.w, cur[i], acc[7]);
         }
     }
 #pragma unroll
@@ -141,9 +165,9 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
 // ----------------------------------------------------------------- experts
 
 constexpr int kN = 16;                 // tokens of a cluster
-constexpr int kThreads = 192;          // producer, MMA, four promotion warps
+constexpr int kThreads = 224;          // producer, MMA, four promotion warps, MMA
 constexpr int kSlot = kBlk * kBlk;     // a ring slot: 16 KB
-constexpr int kMinRing = 2, kMaxRing = 12;
+constexpr int kMinRing = 2, kMaxRing = 12;  // even: each of the two MMA warps keeps to its own slots and buffers
 constexpr int kBufs = 8;               // TMEM buffers of 16 columns
 constexpr int kTmemCols = kBufs * kN;
 constexpr int kUnit = 16;              // hidden features of a lane quarter
@@ -152,6 +176,7 @@ constexpr int kUnit = 16;              // hidden features of a lane quarter
 // [16][features of a rank] | scales of x | scales of the hidden features.
 struct Layout {
     int ring;        // slots
+    int nu[2], no;   // units of 16 features (routed, shared) and of 32 output rows in a tile
     int operand;     // byte offsets
     int hidden, hidden_ld;
     int sx, sh;
@@ -163,8 +188,8 @@ struct ExpertShared {
     uint32_t tmem;
     int abort;
     int count[kMaxExperts];
-    int expert, first, n;    // the cluster's expert (E: shared; -1: none), its first token in the expert's list, tokens
-    int list[kN];            // slot t * k + j (shared: T * k + t)
+    int expert, first, n;    // the cluster's expert (E + i: part i of the shared one; -1: none), its first token in the expert's list, tokens
+    int list[kN];            // slot t * k + j (shared: (k + part) * T + t)
     int token[kN];
     int last[kN];
 };
@@ -193,19 +218,55 @@ __device__ __forceinline__ void add_scaled(float2 (&acc)[kN / 2], const uint32_t
     }
 }
 
+// acc = the sum of KB blocks of the tile whose first step is i: w[kb] s[kb][column] times the step's buffer.  The next
+// buffer's load runs under this one's additions.
+__device__ __forceinline__ bool add_blocks(float2 (&acc)[kN / 2], ExpertShared* sm, uint32_t tl, int i, int KB, const float* w,
+                                           const float* s, int* err, int site) {
+#pragma unroll
+    for (int c = 0; c < kN / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
+    float w0 = w[0], w1 = w[KB > 1 ? 1 : 0];
+    uint32_t v[2][kN];
+    if (!warp_wait(&sm->accf[i % kBufs], (i / kBufs) & 1, &sm->abort, err, site)) return false;
+    tc5::after_sync();
+    tc5::tmem_ld16(tl + i % kBufs * kN, v[0]);
+    for (int kb0 = 0; kb0 < KB; kb0 += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int kb = kb0 + u;
+            if (kb >= KB) break;
+            tc5::tmem_wait_ld(v[u]);
+            tc5::before_sync();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) mbar_arrive(&sm->acce[(i + kb) % kBufs]);
+            const float wc = w0;
+            w0 = w1;
+            if (kb + 2 < KB) w1 = w[kb + 2];
+            if (kb + 1 < KB) {
+                const int n = i + kb + 1;
+                if (!warp_wait(&sm->accf[n % kBufs], (n / kBufs) & 1, &sm->abort, err, site)) return false;
+                tc5::after_sync();
+                tc5::tmem_ld16(tl + n % kBufs * kN, v[u ^ 1]);
+            }
+            add_scaled(acc, v[u], s + kb * kN, wc);
+        }
+    }
+    return true;
+}
+
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdiv_rn(g, 1.0f + expf(-g)) * u; }
 
 // The cluster's expert, tokens and slots (every CTA for itself).
 __device__ __forceinline__ void find_work(const MoePlan& p, ExpertShared* sm, int work, int tid) {
-    const int chunks_sh = (p.T + kN - 1) / kN;
+    const int chunks = (p.T + kN - 1) / kN, chunks_sh = chunks * p.parts;
     if (work < chunks_sh) {  // the shared expert first: the longest clusters
+        const int part = work / chunks, first = (work - part * chunks) * kN;
         if (tid < kN) {
-            sm->token[tid] = work * kN + tid;
-            sm->list[tid] = p.T * p.k + work * kN + tid;
+            sm->token[tid] = first + tid;
+            sm->list[tid] = (p.k + part) * p.T + first + tid;
         }
         if (tid == 0) {
-            sm->expert = p.E;
-            sm->n = min(kN, p.T - work * kN);
+            sm->expert = p.E + part;
+            sm->n = min(kN, p.T - first);
         }
     }
     const bool counts = p.out_counts && blockIdx.x == 0;
@@ -318,50 +379,53 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
         if (warp == 1) tc5::tmem_dealloc(tmem, kTmemCols);
         return;
     }
-    const bool is_shared = expert == p.E;
-    const int n = sm->n, d = p.d, H = is_shared ? p.hs : p.h;
+    const bool is_shared = expert >= p.E;
+    const int n = sm->n, d = p.d;
+    const int part0 = is_shared ? (expert - p.E) * p.part_hidden : 0;  // first hidden feature
+    const int H = is_shared ? min(p.part_hidden, p.hs - part0) : p.h;
     const int KBd = (d + kBlk - 1) / kBlk, KBh = (H + kBlk - 1) / kBlk;
+    const int KBw = is_shared ? (p.hs + kBlk - 1) / kBlk : KBh;        // of the whole expert
     // this rank's hidden features (units of 16) and output rows (units of 32)
     const int u0 = H / kUnit * rank / S, u1 = H / kUnit * (rank + 1) / S;
     const int o0 = d / 32 * rank / S, o1 = d / 32 * (rank + 1) / S;
-    const int gt = (u1 - u0 + 3) / 4, dt = (o1 - o0 + 3) / 4;  // gate/up and down tiles
+    const int nu = lay.nu[is_shared], no = lay.no;
+    const int gt = (u1 - u0 + nu - 1) / nu, dt = (o1 - o0 + no - 1) / no;  // gate/up and down tiles
     const int ngu = gt * KBd, steps = ngu + dt * KBh;
 
     if (warp == 0) {
-        if (lane == 0) {
-            const CUtensorMap* gm = is_shared ? &sgu_map : &gu_map;
-            const CUtensorMap* dm = is_shared ? &sdn_map : &dn_map;
-            const int grow = is_shared ? 0 : expert * 2 * H, drow = is_shared ? 0 : expert * d;
-            int i = 0;
-            for (; i < steps; ++i) {
-                const int s = i % lay.ring;
-                if (i >= lay.ring && !wait(&sm->empty[s], (i / lay.ring - 1) & 1, &sm->abort, p.err, 21)) break;
-                uint8_t* slot = base + s * kSlot;
-                if (i < ngu) {
-                    const int t = i / KBd, kb = i - t * KBd, nu = min(4, u1 - u0 - 4 * t);
-                    mbar_expect_tx(&sm->full[s], (uint32_t)(nu * 2 * kUnit * kBlk));
-                    for (int q = 0; q < nu; ++q) {
-                        const int f = (u0 + 4 * t + q) * kUnit;
-                        tc5::tma_load_2d(slot + q * 2 * kUnit * kBlk, gm, kb * kBlk, grow + f, &sm->full[s]);
-                        tc5::tma_load_2d(slot + (q * 2 + 1) * kUnit * kBlk, gm, kb * kBlk, grow + H + f, &sm->full[s]);
-                    }
+        const CUtensorMap* gm = is_shared ? &sgu_map : &gu_map;
+        const CUtensorMap* dm = is_shared ? &sdn_map : &dn_map;
+        const int e = is_shared ? 0 : expert, unit0 = part0 / kUnit + u0;
+        int i = 0;
+        for (int t = 0, kb = 0; i < steps; ++i) {
+            const int s = i % lay.ring;
+            if (i >= lay.ring && !warp_wait(&sm->empty[s], (i / lay.ring - 1) & 1, &sm->abort, p.err, 21)) break;
+            const bool down = i >= ngu;
+            if (i == ngu) t = kb = 0;
+            if (elect()) {
+                // the rows of a last tile that are another rank's, or past the matrix, come along unused
+                if (down) {
+                    mbar_expect_tx(&sm->full[s], (uint32_t)(no * 32 * kBlk));
+                    tma_load_3d(base + s * kSlot, dm, part0 + kb * kBlk, (o0 + t * no) * 32, e, &sm->full[s]);
                 } else {
-                    const int j = i - ngu, t = j / KBh, kb = j - t * KBh, nu = min(4, o1 - o0 - 4 * t);
-                    mbar_expect_tx(&sm->full[s], (uint32_t)(nu * 32 * kBlk));
-                    for (int q = 0; q < nu; ++q)
-                        tc5::tma_load_2d(slot + q * 32 * kBlk, dm, kb * kBlk, drow + (o0 + 4 * t + q) * 32, &sm->full[s]);
+                    mbar_expect_tx(&sm->full[s], (uint32_t)(nu * 2 * kUnit * kBlk));
+                    tma_load_5d(base + s * kSlot, gm, kb * kBlk, 0, 0, unit0 + t * nu, e, &sm->full[s]);
                 }
             }
-            for (int j = max(i - lay.ring, 0); j < i; ++j) wait_drain(&sm->full[j % lay.ring], (j / lay.ring) & 1);
+            __syncwarp();
+            if (++kb == (down ? KBh : KBd)) {
+                kb = 0;
+                ++t;
+            }
         }
-    } else if (warp == 1) {
-        int i = 0;
-        for (; i < steps; ++i) {
+        for (int j = max(i - lay.ring, 0); j < i; ++j) wait_drain(&sm->full[j % lay.ring], (j / lay.ring) & 1);
+    } else if (warp == 1 || warp == 6) {
+        int last = -1;
+        for (int i = warp == 1 ? 0 : 1; i < steps; i += 2) {
             const int s = i % lay.ring, b = i % kBufs;
-            if ((i == 0 && gt > 0 && !warp_wait(&sm->xready, 0, &sm->abort, p.err, 22)) ||
-                (i == ngu && !warp_wait(&sm->hready, 0, &sm->abort, p.err, 23)) ||
-                !warp_wait(&sm->full[s], (i / lay.ring) & 1, &sm->abort, p.err, 24) ||
-                !warp_wait(&sm->acce[b], (i / kBufs) & 1, &sm->abort, p.err, 25))
+            if ((i < 2 && gt > 0 && !warp_wait(&sm->xready, 0, &sm->abort, p.err, 22)) ||
+                ((i == ngu || i == ngu + 1) && !warp_wait(&sm->hready, 0, &sm->abort, p.err, 23)) ||
+                !warp_wait2(&sm->full[s], (i / lay.ring) & 1, &sm->acce[b], (i / kBufs) & 1, &sm->abort, p.err, 24))
                 break;
             tc5::after_sync();
             const int kb = i < ngu ? i % KBd : (i - ngu) % KBh;
@@ -375,53 +439,49 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
                 tc5::commit(&sm->accf[b]);
             }
             __syncwarp();
+            last = i;
         }
-        if (i > 0) wait_drain(&sm->accf[(i - 1) % kBufs], ((i - 1) / kBufs) & 1);
+        if (last >= 0) wait_drain(&sm->accf[last % kBufs], (last / kBufs) & 1);
     } else {
         const int pt = tid - 64, quarter = warp & 3, hl = pt & 15;
         const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
         if (lane == 0)
             for (int b = 0; b < kBufs; ++b) mbar_arrive(&sm->acce[b]);
         // the tokens' codes and scales; features past d are zeros
-        for (int i = pt; i < n * KBd * 8; i += 128) {
-            const int t = i / (KBd * 8), c = i - t * KBd * 8;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (c * 16 < d) v = *reinterpret_cast<const uint4*>(p.xq + (int64_t)sm->token[t] * d + c * 16);
-            *reinterpret_cast<uint4*>(operand_at(operand, c >> 3, t, (c & 7) * 16)) = v;
+        if ((pt >> 3) < n) {
+            const int t = pt >> 3, c = pt & 7;  // a 16-byte chunk of a token's blocks, eight blocks in flight
+            const uint8_t* from = p.xq + (int64_t)sm->token[t] * d + c * 16;
+            for (int kb0 = 0; kb0 < KBd; kb0 += 8) {
+                uint4 v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    v[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if ((kb0 + u) * kBlk + c * 16 < d) v[u] = *reinterpret_cast<const uint4*>(from + (kb0 + u) * kBlk);
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (kb0 + u < KBd) *reinterpret_cast<uint4*>(operand_at(operand, kb0 + u, t, c * 16)) = v[u];
+            }
         }
-        for (int i = pt; i < n * KBd; i += 128) {
-            const int t = i / KBd, kb = i - t * KBd;
-            sx[kb * kN + t] = p.sx[sm->token[t] * KBd + kb];
+        if ((pt & 15) < n) {
+            const float* from = p.sx + sm->token[pt & 15] * KBd;
+#pragma unroll 4
+            for (int kb = pt >> 4; kb < KBd; kb += 8) sx[kb * kN + (pt & 15)] = from[kb];
         }
         fence_async_smem();
         mbar_arrive(&sm->xready);
         bool ok = warp_wait(&sm->xready, 0, &sm->abort, p.err, 26);
         int i = 0;
         // gate and up: a lane holds one weight row; lanes l and l + 16 the gate and up rows of a feature
-        const float* sgu = is_shared ? p.sh_s_gate_up : p.s_gate_up + (int64_t)expert * 2 * KBh * KBd;
+        const float* sgu = is_shared ? p.sh_s_gate_up + (int64_t)(part0 / kBlk) * KBd : p.s_gate_up + (int64_t)expert * 2 * KBh * KBd;
         for (int t = 0; t < gt && ok; ++t) {
-            const int unit = u0 + 4 * t + quarter;
-            const bool mine = unit < u1;
-            const float* sw = sgu + (int64_t)((lane < 16 ? 0 : KBh) + (mine ? unit * kUnit / kBlk : 0)) * KBd;
+            const int unit = u0 + nu * t + quarter;
+            const bool mine = quarter < nu && unit < u1;
+            const float* sw = sgu + (int64_t)((lane < 16 ? 0 : KBw) + (mine ? unit * kUnit / kBlk : 0)) * KBd;
             float2 acc[kN / 2];
-#pragma unroll
-            for (int c = 0; c < kN / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
-            float w = sw[0];
-            for (int kb = 0; kb < KBd; ++kb, ++i) {
-                const int b = i % kBufs;
-                const float wc = w;
-                if (kb + 1 < KBd) w = sw[kb + 1];
-                ok = warp_wait(&sm->accf[b], (i / kBufs) & 1, &sm->abort, p.err, 27);
-                if (!ok) break;
-                tc5::after_sync();
-                uint32_t v[kN];
-                tc5::tmem_ld16(tl + b * kN, v);
-                tc5::tmem_wait_ld(v);
-                tc5::before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm->acce[b]);
-                add_scaled(acc, v, sx + kb * kN, wc);
-            }
+            ok = add_blocks(acc, sm, tl, i, KBd, sw, sx, p.err, 27);
+            i += KBd;
+            if (!ok) break;
             // lanes below 16 finish the even tokens, the others the odd ones
             const int f = (unit - u0) * kUnit + (lane & 15);
 #pragma unroll
@@ -441,52 +501,49 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
             wait_cluster(&sm->peers, 0, &sm->abort, p.err, 32);  // each lane's own acquire
         }
         if (dt > 0 && ok) {
-            for (int j = pt >> 4; j < n * KBh; j += 8) {
-                const int t = j / KBh, kb = j - t * KBh, f = kb * kBlk + hl * 8;
-                float v[8] = {};
-                if (f < H) {
-                    // the rank that owns unit f / 16: the last one that starts at or before it
-                    const int u = f / kUnit, r = (S * (u + 1) - 1) / (H / kUnit);
-                    const uint32_t at = peer_addr(hidden + t * lay.hidden_ld + (f - H / kUnit * r / S * kUnit), (uint32_t)r);
-                    const float4 a = peer_load4(at), b = peer_load4(at + 16);
-                    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-                    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-                }
-                uint32_t am = amax8(v);  // the half warps of a warp may part at the end of the loop
+            // a half warp per (token, block), four of them in flight
+            const int U = H / kUnit, items = n * KBh;
+            const float inv = __fdividef(1.0f, (float)KBh);
+            // (both half warps of a warp make the same turns: they meet in the shuffles)
+            for (int jw = pt >> 5 << 1; jw < items; jw += 32) {
+                float4 a[4], b[4];
+                int t[4], kb[4];
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffu << (threadIdx.x & 16), am, o));
-                const float s = scale_of(am);
-                *reinterpret_cast<uint2*>(operand_at(operand, kb, t, hl * 8)) = Coder(s)(v);
-                if (hl == 0) sh[kb * kN + t] = s;
+                for (int u = 0; u < 4; ++u) {
+                    a[u] = b[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (jw + 8 * u >= items) continue;
+                    const int j = min(jw + (pt >> 4 & 1) + 8 * u, items - 1);  // the last one may be read by both
+                    t[u] = (int)(((float)j + 0.5f) * inv);                     // exact: j is at most 16 * 32
+                    kb[u] = j - t[u] * KBh;
+                    const int f = kb[u] * kBlk + hl * 8;
+                    if (f < H) {
+                        // the rank that owns unit f / 16: the last one that starts at or before it
+                        const int r = (S * (f / kUnit + 1) - 1) / U;
+                        const uint32_t at = peer_addr(hidden + t[u] * lay.hidden_ld + (f - U * r / S * kUnit), (uint32_t)r);
+                        a[u] = peer_load4(at);
+                        b[u] = peer_load4(at + 16);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (jw + 8 * u >= items) continue;
+                    const float v[8] = {a[u].x, a[u].y, a[u].z, a[u].w, b[u].x, b[u].y, b[u].z, b[u].w};
+                    const float s = scale_of(half_warp_max(amax8(v)));
+                    *reinterpret_cast<uint2*>(operand_at(operand, kb[u], t[u], hl * 8)) = Coder(s)(v);
+                    if (hl == 0) sh[kb[u] * kN + t[u]] = s;
+                }
             }
         }
         fence_async_smem();
         mbar_arrive(&sm->hready);
         ok = warp_wait(&sm->hready, 0, &sm->abort, p.err, 28) && ok;
-        const float* sdn = is_shared ? p.sh_s_down : p.s_down + (int64_t)expert * KBd * KBh;
+        const float* sdn = is_shared ? p.sh_s_down + part0 / kBlk : p.s_down + (int64_t)expert * KBd * KBh;
         for (int t = 0; t < dt && ok; ++t) {
-            const int og = o0 + 4 * t + quarter;
-            const bool mine = og < o1;
-            const float* sw = sdn + (int64_t)(mine ? og * 32 / kBlk : 0) * KBh;
+            const int og = o0 + no * t + quarter;
+            const bool mine = quarter < no && og < o1;
             float2 acc[kN / 2];
-#pragma unroll
-            for (int c = 0; c < kN / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
-            float w = sw[0];
-            for (int kb = 0; kb < KBh; ++kb, ++i) {
-                const int b = i % kBufs;
-                const float wc = w;
-                if (kb + 1 < KBh) w = sw[kb + 1];
-                ok = warp_wait(&sm->accf[b], (i / kBufs) & 1, &sm->abort, p.err, 29);
-                if (!ok) break;
-                tc5::after_sync();
-                uint32_t v[kN];
-                tc5::tmem_ld16(tl + b * kN, v);
-                tc5::tmem_wait_ld(v);
-                tc5::before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm->acce[b]);
-                add_scaled(acc, v, sh + kb * kN, wc);
-            }
+            ok = add_blocks(acc, sm, tl, i, KBh, sdn + (int64_t)(mine ? og * 32 / kBlk : 0) * KBw, sh, p.err, 29);
+            i += KBh;
             if (!ok || !mine) continue;
             const int col = og * 32 + lane;
 #pragma unroll
@@ -501,7 +558,7 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
         if (lane == 0) mbar_arrive(&sm->pbar);
         ok = warp_wait(&sm->pbar, 0, &sm->abort, p.err, 30) && ok;
         if (ok && o1 > o0) {
-            if (pt < n) sm->last[pt] = atomicAdd(&p.arrived[sm->token[pt] * 16 + rank], 1u) == (uint32_t)p.k;
+            if (pt < n) sm->last[pt] = atomicAdd(&p.arrived[sm->token[pt] * kRanks + rank], 1u) == (uint32_t)(p.k + p.parts - 1);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->pbar);
             ok = warp_wait(&sm->pbar, 1, &sm->abort, p.err, 31);
@@ -517,6 +574,7 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
 #pragma unroll
                     for (int q = 0; q < kMaxTopK; ++q) v[q] = q < p.k ? __ldcg(row + (int64_t)q * d + col) : 0.0f;
                     float sum = __ldcg(shr + col);
+                    for (int q = 1; q < p.parts; ++q) sum += __ldcg(shr + (int64_t)q * p.T * d + col);
 #pragma unroll
                     for (int q = 0; q < kMaxTopK; ++q)
                         if (q < p.k) sum = fmaf(gate[q], v[q], sum);
@@ -537,15 +595,24 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
 }
 
 // Ring slots and offsets for a cluster of S; at least two CTAs an SM where that leaves four slots each.
+// Of `all` units, dealt to S ranks: how many a tile takes (4 at most, none more than a rank needs).
+int tile_units(int all, int S) {
+    const int most = (all + S - 1) / S, tiles = (most + 3) / 4;
+    return (most + tiles - 1) / tiles;
+}
+
 Layout layout_for(const MoePlan& p, int S) {
-    const int hm = std::max(p.h, p.hs), KBd = (int)blocks_of(p.d), KBh = (int)blocks_of(hm);
+    const int hm = std::max(p.h, std::min(p.part_hidden, p.hs)), KBd = (int)blocks_of(p.d), KBh = (int)blocks_of(hm);
     Layout l = {};
+    l.nu[0] = tile_units(p.h / kUnit, S);
+    l.nu[1] = tile_units(std::min(p.part_hidden, p.hs) / kUnit, S);
+    l.no = tile_units(p.d / 32, S);
     l.hidden_ld = (hm / kUnit + S - 1) / S * kUnit;
     const int operand = std::max(KBd, KBh) * kN * kBlk, hidden = kN * l.hidden_ld * 4;
     const int rest = operand + hidden + (KBd + KBh) * kN * 4;
     const int half = 113 * 1024 - 2048 - 1024, whole = 226 * 1024 - 2048 - 1024;  // less static shared memory and alignment
     const int room = (half - rest) / kSlot >= 4 ? half : whole;
-    l.ring = std::min((room - rest) / kSlot, kMaxRing);
+    l.ring = std::min((room - rest) / kSlot, kMaxRing) / 2 * 2;
     l.operand = l.ring * kSlot;
     l.hidden = l.operand + operand;
     l.sx = l.hidden + hidden;
@@ -554,12 +621,34 @@ Layout layout_for(const MoePlan& p, int S) {
     return l;
 }
 
+// Gate and up rows: (k, row of a unit, gate or up, unit, expert), so that one copy brings a tile as the kernel wants it.
+cudaError_t gate_up_map(CUtensorMap* m, const uint8_t* w, int d, int H, int E, int nu) {
+    const uint64_t D = (uint64_t)d;
+    const uint64_t dims[5] = {D, kUnit, 2, (uint64_t)(H / kUnit), (uint64_t)E};
+    const uint64_t strides[4] = {D, (uint64_t)H * D, kUnit * D, 2 * (uint64_t)H * D};
+    const uint32_t box[5] = {kBlk, kUnit, 2, (uint32_t)nu, 1};
+    return byte_map_n(m, w, 5, dims, strides, box);
+}
+cudaError_t down_map(CUtensorMap* m, const uint8_t* w, int d, int H, int E, int no) {
+    const uint64_t dims[3] = {(uint64_t)H, (uint64_t)d, (uint64_t)E};
+    const uint64_t strides[2] = {(uint64_t)H, (uint64_t)d * (uint64_t)H};
+    const uint32_t box[3] = {kBlk, (uint32_t)(32 * no), 1};
+    return byte_map_n(m, w, 3, dims, strides, box);
+}
+
 template <int S>
-cudaError_t launch_experts(const MoePlan& p, const CUtensorMap* m, int clusters, cudaStream_t st) {
+cudaError_t launch_experts(const MoePlan& p, int clusters, cudaStream_t st) {
+    static_assert(S <= kRanks, "one counter a rank");
     const Layout l = layout_for(p, S);
     if (l.ring < kMinRing) return cudaErrorInvalidValue;
+    CUtensorMap m[4];
+    cudaError_t e = gate_up_map(&m[0], p.gate_up, p.d, p.h, p.E, l.nu[0]);
+    if (e == cudaSuccess) e = down_map(&m[1], p.down, p.d, p.h, p.E, l.no);
+    if (e == cudaSuccess) e = gate_up_map(&m[2], p.sh_gate_up, p.d, p.hs, 1, l.nu[1]);
+    if (e == cudaSuccess) e = down_map(&m[3], p.sh_down, p.d, p.hs, 1, l.no);
+    if (e != cudaSuccess) return e;
     auto kern = moe_experts_kernel<S>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, l.bytes + 1024);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, l.bytes + 1024);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * S));
@@ -581,6 +670,9 @@ cudaError_t launch_experts(const MoePlan& p, const CUtensorMap* m, int clusters,
 }  // namespace
 
 size_t carve_moe(MoePlan& p, unsigned char* base) {
+    // the shared expert in parts no wider than a routed one, of whole quantisation blocks
+    p.part_hidden = (int)blocks_of(p.h) * kBlk;
+    p.parts = (p.hs + p.part_hidden - 1) / p.part_hidden;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         unsigned char* q = base ? base + off : nullptr;
@@ -590,22 +682,18 @@ size_t carve_moe(MoePlan& p, unsigned char* base) {
     const size_t T = (size_t)p.T, k = (size_t)p.k, d = (size_t)p.d;
     p.idx = static_cast<int32_t*>(take(T * k * 4));
     p.gate = static_cast<float*>(take(T * k * 4));
-    p.arrived = static_cast<uint32_t*>(take(T * 16 * 4));
+    p.arrived = static_cast<uint32_t*>(take(T * kRanks * 4));
     p.sx = static_cast<float*>(take(T * (size_t)blocks_of(p.d) * 4));
     p.xq = static_cast<uint8_t*>(take(T * d));
-    p.part = static_cast<float*>(take(T * (k + 1) * d * 4));
+    p.part = static_cast<float*>(take(T * (k + (size_t)p.parts) * d * 4));
     return off;
 }
 
 cudaError_t launch_moe_few(const MoePlan& p, cudaStream_t st) {
-    CUtensorMap m[4];
-    cudaError_t e = byte_map(&m[0], p.gate_up, (uint64_t)p.d, (uint64_t)p.E * 2 * p.h, (uint64_t)p.d, kUnit);
-    if (e == cudaSuccess) e = byte_map(&m[1], p.down, (uint64_t)p.h, (uint64_t)p.E * p.d, (uint64_t)p.h, 32);
-    if (e == cudaSuccess) e = byte_map(&m[2], p.sh_gate_up, (uint64_t)p.d, (uint64_t)2 * p.hs, (uint64_t)p.d, kUnit);
-    if (e == cudaSuccess) e = byte_map(&m[3], p.sh_down, (uint64_t)p.hs, (uint64_t)p.d, (uint64_t)p.hs, 32);
-    if (e != cudaSuccess) return e;
     const int ks = 32 * ((p.d / 32 + kRouteCluster - 1) / kRouteCluster);
     const size_t smem = (size_t)kRouteCluster * ks * 4;
+    cudaError_t e = cudaFuncSetAttribute(moe_route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((p.T + kRouteCluster - 1) / kRouteCluster * kRouteCluster));
     cfg.blockDim = dim3(kRouteThreads);
@@ -620,8 +708,8 @@ cudaError_t launch_moe_few(const MoePlan& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     // clusters at most: the shared expert's chunks, an expert per slot, and a chunk more per 16 slots
     const int slots = p.T * p.k;
-    const int clusters = (p.T + kN - 1) / kN + std::min(p.E, slots) + slots / kN;
-    return launch_experts<8>(p, m, clusters, st);
+    const int clusters = (p.T + kN - 1) / kN * p.parts + std::min(p.E, slots) + slots / kN;
+    return launch_experts<8>(p, clusters, st);
 }
 
 }  // namespace f8
