@@ -58,6 +58,8 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
     extern __shared__ float route_smem[];          // x slice [ks][8]
     __shared__ float red[kRouteParts][kRouteCluster][kMaxExperts];
     __shared__ float part[kRouteCluster][kMaxExperts];
+    __shared__ int32_t top_idx[kMaxTopK];
+    __shared__ float top_gate[kMaxTopK];
     const int tid = threadIdx.x, rank = (int)cluster_rank();
     const int t0 = (blockIdx.x / kRouteCluster) * kRouteCluster;
     const int nt = min(kRouteCluster, p.T - t0);
@@ -83,22 +85,7 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
 #pragma unroll
         for (int j = 0; j < 8; ++j) route_smem[(c + j) * kRouteCluster + t] = v[j];
     }
-    // codes and scales of token t0 + rank, and its counters
     const int mt = t0 + rank;
-    const int KB = (p.d + kBlk - 1) / kBlk;
-    if (rank < nt) {
-        const int hl = tid & 15;
-        for (int b0 = 0; b0 < KB; b0 += kRouteThreads / 16) {
-            const int b = b0 + (tid >> 4), c = b * kBlk + hl * 8;
-            float v[8] = {};
-            if (b < KB && c < p.d) load8(p.x + (int64_t)mt * p.d + c, v);
-            const float s = scale_of(half_warp_max(amax8(v)));
-            if (b < KB && c < p.d)
-                *reinterpret_cast<uint2*>(p.xq + (int64_t)mt * p.d + c) = Coder(s)(v);
-            if (b < KB && hl == 0) p.sx[mt * KB + b] = s;
-        }
-        if (tid < kRanks) p.arrived[mt * kRanks + tid] = 0;
-    }
     __syncthreads();
     float acc[kRouteCluster] = {};
     for (int i0 = 0; i0 < n; i0 += kRouteAhead * kRouteParts) {
@@ -150,12 +137,27 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
         g.router_bias = p.router_bias;
         l0 = tid < p.E ? biased_logit(g, l0, tid) : -INFINITY;
         l1 = tid + 32 < p.E ? biased_logit(g, l1, tid + 32) : -INFINITY;
-        gate_topk_warp(g, p.router_bias, mt, l0, l1, tid, p.idx, p.gate, nullptr);
+        gate_topk_warp(g, p.router_bias, 0, l0, l1, tid, top_idx, top_gate, nullptr);
         __syncwarp();
         if (tid < p.k) {
-            if (p.out_idx) p.out_idx[mt * p.k + tid] = p.idx[mt * p.k + tid];
-            if (p.out_gate) p.out_gate[mt * p.k + tid] = p.gate[mt * p.k + tid];
+            p.idx[mt * p.k + tid] = top_idx[tid];
+            p.gate[mt * p.k + tid] = top_gate[tid];
+            if (p.out_idx) p.out_idx[mt * p.k + tid] = top_idx[tid];
+            if (p.out_gate) p.out_gate[mt * p.k + tid] = top_gate[tid];
         }
+    } else if (rank < nt) {
+        // beside the top-k, the other warps: codes and scales of token t0 + rank, and its counters
+        constexpr int kHalfWarps = kRouteThreads / 16 - 2;
+        const int KB = (p.d + kBlk - 1) / kBlk, hl = tid & 15;
+        for (int b0 = 0; b0 < KB; b0 += kHalfWarps) {
+            const int b = b0 + (tid >> 4) - 2, c = b * kBlk + hl * 8;
+            float v[8] = {};
+            if (b < KB && c < p.d) load8(p.x + (int64_t)mt * p.d + c, v);
+            const float s = scale_of(half_warp_max(amax8(v)));
+            if (b < KB && c < p.d) *reinterpret_cast<uint2*>(p.xq + (int64_t)mt * p.d + c) = Coder(s)(v);
+            if (b < KB && hl == 0) p.sx[mt * KB + b] = s;
+        }
+        if (tid < 32 + kRanks) p.arrived[mt * kRanks + tid - 32] = 0;
     }
     // the partial logits stay until every CTA has read them
     cluster_arrive();
@@ -171,6 +173,7 @@ constexpr int kMinRing = 2, kMaxRing = 12;  // even: each of the two MMA warps k
 constexpr int kBufs = 8;               // TMEM buffers of 16 columns
 constexpr int kTmemCols = kBufs * kN;
 constexpr int kUnit = 16;              // hidden features of a lane quarter
+constexpr int kAlone = 16;             // (token, block) items that each CTA quantises for itself
 
 // Dynamic shared memory: ring | operand codes (x, then the hidden features) | own hidden features
 // [16][features of a rank] | scales of x | scales of the hidden features.
@@ -184,10 +187,11 @@ struct Layout {
 };
 
 struct ExpertShared {
-    uint64_t full[kMaxRing], empty[kMaxRing], accf[kBufs], acce[kBufs], xready, hready, pbar, peers;
+    uint64_t full[kMaxRing], empty[kMaxRing], accf[kBufs], acce[kBufs], xready, hready, pbar, peers, codes;
     uint32_t tmem;
     int abort;
     int count[kMaxExperts];
+    uint8_t slot[kFewTokens * kMaxTopK];  // the expert of each (token, choice)
     int expert, first, n;    // the cluster's expert (E + i: part i of the shared one; -1: none), its first token in the expert's list, tokens
     int list[kN];            // slot t * k + j (shared: (k + part) * T + t)
     int token[kN];
@@ -201,6 +205,13 @@ __device__ __forceinline__ float4 peer_load4(uint32_t addr) {
                  : "r"(addr)
                  : "memory");
     return v;
+}
+
+__device__ __forceinline__ void peer_store8(uint32_t addr, uint2 v) {
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+}
+__device__ __forceinline__ void peer_store(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // 16-byte chunk c of operand row t lies at chunk c ^ (t & 7) (128-byte swizzle).
@@ -218,13 +229,15 @@ __device__ __forceinline__ void add_scaled(float2 (&acc)[kN / 2], const uint32_t
     }
 }
 
-// acc = the sum of KB blocks of the tile whose first step is i: w[kb] s[kb][column] times the step's buffer.  The next
-// buffer's load runs under this one's additions.
+__device__ __forceinline__ float2 first_two(const float* w, int KB) { return make_float2(w[0], w[KB > 1 ? 1 : 0]); }
+
+// acc = the sum of KB blocks of the tile whose first step is i: w[kb] s[kb][column] times the step's buffer, w01 being
+// first_two(w, KB), read ahead.  The next buffer's load runs under this one's additions.
 __device__ __forceinline__ bool add_blocks(float2 (&acc)[kN / 2], ExpertShared* sm, uint32_t tl, int i, int KB, const float* w,
-                                           const float* s, int* err, int site) {
+                                           float2 w01, const float* s, int* err, int site) {
 #pragma unroll
     for (int c = 0; c < kN / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
-    float w0 = w[0], w1 = w[KB > 1 ? 1 : 0];
+    float w0 = w01.x, w1 = w01.y;
     uint32_t v[2][kN];
     if (!warp_wait(&sm->accf[i % kBufs], (i / kBufs) & 1, &sm->abort, err, site)) return false;
     tc5::after_sync();
@@ -275,7 +288,35 @@ __device__ __forceinline__ void find_work(const MoePlan& p, ExpertShared* sm, in
         return;
     }
     const int S = p.T * p.k;
-    for (int i = tid; i < S; i += kThreads) atomicAdd(&sm->count[p.idx[i]], 1);
+    if (S <= 32 && p.T <= kN && !counts) {
+        // a lane a choice: cluster j takes the j-th expert in the order of their first choice (no more than kN tokens
+        // have it)
+        if (tid < 32) {
+            const int e = tid < S ? p.idx[tid] : -1;
+            const unsigned same = __match_any_sync(0xffffffffu, e);
+            unsigned firsts = __ballot_sync(0xffffffffu, e >= 0 && __ffs(same) - 1 == tid);
+            for (int j = work - chunks_sh; j > 0 && firsts; --j) firsts &= firsts - 1;
+            const int pick = __ffs(firsts) - 1;
+            const int expert = __shfl_sync(0xffffffffu, e, max(pick, 0));
+            const unsigned mine = __shfl_sync(0xffffffffu, same, max(pick, 0));
+            if (pick >= 0 && (mine >> tid & 1)) {
+                const int at = __popc(mine & ((1u << tid) - 1u));
+                sm->list[at] = tid;
+                sm->token[at] = tid / p.k;
+            }
+            if (tid == 0) {
+                sm->expert = pick >= 0 ? expert : -1;
+                sm->n = __popc(mine);
+            }
+        }
+        __syncthreads();
+        return;
+    }
+    for (int i = tid; i < S; i += kThreads) {
+        const int e = p.idx[i];
+        sm->slot[i] = (uint8_t)e;
+        atomicAdd(&sm->count[e], 1);
+    }
     __syncthreads();
     if (counts) {
         for (int e = tid; e < p.E; e += kThreads) p.out_counts[e] = sm->count[e];
@@ -315,7 +356,7 @@ __device__ __forceinline__ void find_work(const MoePlan& p, ExpertShared* sm, in
             int seen = 0;
             for (int i0 = 0; i0 < S && seen < first + kN; i0 += 32) {
                 const int i = i0 + tid;
-                const bool hit = i < S && p.idx[i] == e;
+                const bool hit = i < S && sm->slot[i] == e;
                 const unsigned m = __ballot_sync(0xffffffffu, hit);
                 const int at = seen + __popc(m & ((1u << tid) - 1u)) - first;
                 if (hit && at >= 0 && at < kN) {
@@ -358,10 +399,17 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
         mbar_init(&sm->hready, 128);
         mbar_init(&sm->pbar, 4);
         mbar_init(&sm->peers, S * 4);
+        mbar_init(&sm->codes, S * 4);
         sm->abort = 0;
         async::fence_barrier_init();
     }
     if (tid < kMaxExperts) sm->count[tid] = 0;
+    if (tid == 64) {
+        prefetch_map(&gu_map);
+        prefetch_map(&dn_map);
+        prefetch_map(&sgu_map);
+        prefetch_map(&sdn_map);
+    }
     if (warp == 1) {
         tc5::tmem_alloc(&sm->tmem, kTmemCols);
         tc5::before_sync();
@@ -447,6 +495,19 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
         const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
         if (lane == 0)
             for (int b = 0; b < kBufs; ++b) mbar_arrive(&sm->acce[b]);
+        // where this thread's weight scales lie, the first of them read before anything else
+        const float* sgu = is_shared ? p.sh_s_gate_up + (int64_t)(part0 / kBlk) * KBd : p.s_gate_up + (int64_t)expert * 2 * KBh * KBd;
+        const auto gate_up_scales = [&](int t) {
+            const int unit = u0 + nu * t + quarter;
+            const bool mine = quarter < nu && unit < u1;
+            return sgu + (int64_t)((lane < 16 ? 0 : KBw) + (mine ? unit * kUnit / kBlk : 0)) * KBd;
+        };
+        const float* sdn = is_shared ? p.sh_s_down + part0 / kBlk : p.s_down + (int64_t)expert * KBd * KBh;
+        const auto down_scales = [&](int t) {
+            const int og = o0 + no * t + quarter;
+            return sdn + (int64_t)(quarter < no && og < o1 ? og * 32 / kBlk : 0) * KBw;
+        };
+        float2 gate_up_w = first_two(gate_up_scales(0), KBd), down_w = first_two(down_scales(0), KBh);
         // the tokens' codes and scales; features past d are zeros
         if ((pt >> 3) < n) {
             const int t = pt >> 3, c = pt & 7;  // a 16-byte chunk of a token's blocks, eight blocks in flight
@@ -473,13 +534,13 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
         bool ok = warp_wait(&sm->xready, 0, &sm->abort, p.err, 26);
         int i = 0;
         // gate and up: a lane holds one weight row; lanes l and l + 16 the gate and up rows of a feature
-        const float* sgu = is_shared ? p.sh_s_gate_up + (int64_t)(part0 / kBlk) * KBd : p.s_gate_up + (int64_t)expert * 2 * KBh * KBd;
         for (int t = 0; t < gt && ok; ++t) {
             const int unit = u0 + nu * t + quarter;
             const bool mine = quarter < nu && unit < u1;
-            const float* sw = sgu + (int64_t)((lane < 16 ? 0 : KBw) + (mine ? unit * kUnit / kBlk : 0)) * KBd;
             float2 acc[kN / 2];
-            ok = add_blocks(acc, sm, tl, i, KBd, sw, sx, p.err, 27);
+            const float2 w01 = gate_up_w;
+            if (t + 1 < gt) gate_up_w = first_two(gate_up_scales(t + 1), KBd);
+            ok = add_blocks(acc, sm, tl, i, KBd, gate_up_scales(t), w01, sx, p.err, 27);
             i += KBd;
             if (!ok) break;
             // lanes below 16 finish the even tokens, the others the odd ones
@@ -500,49 +561,68 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
             ok = __shfl_sync(0xffffffffu, ok, 0);
             wait_cluster(&sm->peers, 0, &sm->abort, p.err, 32);  // each lane's own acquire
         }
-        if (dt > 0 && ok) {
-            // a half warp per (token, block), four of them in flight
-            const int U = H / kUnit, items = n * KBh;
+        if (ok) {
+            // A half warp per (token, block), four of them in flight.  With few of them each CTA quantises all for
+            // itself; with more, 1 / S of them for all, at the price of another signal (about 1 us): 128 items took
+            // 8.6 us alone and take 4.0 us shared.
+            const int U = H / kUnit, items = n * KBh, stride = items > kAlone ? S : 1, first = items > kAlone ? rank : 0;
+            const int own = (items - first + stride - 1) / stride;
             const float inv = __fdividef(1.0f, (float)KBh);
             // (both half warps of a warp make the same turns: they meet in the shuffles)
-            for (int jw = pt >> 5 << 1; jw < items; jw += 32) {
+            for (int jw = pt >> 5 << 1; jw < own; jw += 32) {
                 float4 a[4], b[4];
-                int t[4], kb[4];
+                int at[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     a[u] = b[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (jw + 8 * u >= items) continue;
-                    const int j = min(jw + (pt >> 4 & 1) + 8 * u, items - 1);  // the last one may be read by both
-                    t[u] = (int)(((float)j + 0.5f) * inv);                     // exact: j is at most 16 * 32
-                    kb[u] = j - t[u] * KBh;
-                    const int f = kb[u] * kBlk + hl * 8;
+                    if (jw + 8 * u >= own) continue;
+                    const int j = first + stride * min(jw + (pt >> 4 & 1) + 8 * u, own - 1);  // the last one may be read by both
+                    const int t = (int)(((float)j + 0.5f) * inv), kb = j - t * KBh;         // exact: j is at most 16 * 32
+                    const int f = kb * kBlk + hl * 8;
+                    at[u] = kb * kN + t;
                     if (f < H) {
                         // the rank that owns unit f / 16: the last one that starts at or before it
                         const int r = (S * (f / kUnit + 1) - 1) / U;
-                        const uint32_t at = peer_addr(hidden + t[u] * lay.hidden_ld + (f - U * r / S * kUnit), (uint32_t)r);
-                        a[u] = peer_load4(at);
-                        b[u] = peer_load4(at + 16);
+                        const uint32_t from = peer_addr(hidden + t * lay.hidden_ld + (f - U * r / S * kUnit), (uint32_t)r);
+                        a[u] = peer_load4(from);
+                        b[u] = peer_load4(from + 16);
                     }
                 }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    if (jw + 8 * u >= items) continue;
+                    if (jw + 8 * u >= own) continue;
                     const float v[8] = {a[u].x, a[u].y, a[u].z, a[u].w, b[u].x, b[u].y, b[u].z, b[u].w};
                     const float s = scale_of(half_warp_max(amax8(v)));
-                    *reinterpret_cast<uint2*>(operand_at(operand, kb[u], t[u], hl * 8)) = Coder(s)(v);
-                    if (hl == 0) sh[kb[u] * kN + t[u]] = s;
+                    const uint2 code = Coder(s)(v);
+                    uint8_t* to = operand + at[u] * kBlk + (((hl >> 1) ^ (at[u] & 7)) << 4) + (hl & 1) * 8;
+                    if (stride == 1) {
+                        *reinterpret_cast<uint2*>(to) = code;
+                        if (hl == 0) sh[at[u]] = s;
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < S; ++r) peer_store8(peer_addr(to, (uint32_t)r), code);
+                        if (hl < S) peer_store(peer_addr(sh + at[u], (uint32_t)hl), s);
+                    }
                 }
+            }
+            if (stride != 1) {
+                __syncwarp();
+                if (lane < S) peer_arrive(peer_addr(&sm->codes, (uint32_t)lane));
+                if (lane == 0) ok = wait_cluster(&sm->codes, 0, &sm->abort, p.err, 33);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                wait_cluster(&sm->codes, 0, &sm->abort, p.err, 33);  // each lane's own acquire
             }
         }
         fence_async_smem();
         mbar_arrive(&sm->hready);
         ok = warp_wait(&sm->hready, 0, &sm->abort, p.err, 28) && ok;
-        const float* sdn = is_shared ? p.sh_s_down + part0 / kBlk : p.s_down + (int64_t)expert * KBd * KBh;
         for (int t = 0; t < dt && ok; ++t) {
             const int og = o0 + no * t + quarter;
             const bool mine = quarter < no && og < o1;
             float2 acc[kN / 2];
-            ok = add_blocks(acc, sm, tl, i, KBh, sdn + (int64_t)(mine ? og * 32 / kBlk : 0) * KBw, sh, p.err, 29);
+            const float2 w01 = down_w;
+            if (t + 1 < dt) down_w = first_two(down_scales(t + 1), KBh);
+            ok = add_blocks(acc, sm, tl, i, KBh, down_scales(t), w01, sh, p.err, 29);
             i += KBh;
             if (!ok || !mine) continue;
             const int col = og * 32 + lane;
