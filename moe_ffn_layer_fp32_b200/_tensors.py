@@ -1,8 +1,6 @@
 """What the operators' wrappers share: devices, streams and checks of tensors."""
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import _lib
@@ -23,32 +21,51 @@ def need(ok: bool, message: str) -> None:
 
 def same_device(x: torch.Tensor, *others) -> None:
     """x is a CUDA tensor and the others (None is skipped) are on its device."""
-    need(x.is_cuda, "tensors must be CUDA tensors")
+    at = x.get_device()
+    if at < 0 or not x.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
     for t in others:
-        if t is not None and t.device != x.device:
+        if t is not None and t.get_device() != at:
             raise ValueError(f"tensors on {x.device} and {t.device}: one device is needed")
 
 
-def rows_of(t: torch.Tensor, cols: int, name: str) -> None:
-    """t is [rows, cols] with unit stride along the row and rows that do not overlap."""
-    need(t.dim() == 2 and t.shape[1] == cols and (cols == 1 or t.stride(1) == 1)
-         and (t.shape[0] <= 1 or t.stride(0) >= cols), f"{name} must be [rows, {cols}] with contiguous rows")
+def rows_of(t: torch.Tensor, cols: int, name: str) -> int:
+    """t is [rows, cols] with unit stride along the row and rows that do not overlap; the elements between rows."""
+    if t.dim() == 2:
+        (rows, n), (step, unit) = t.shape, t.stride()
+        if n == cols and (unit == 1 or cols == 1):
+            if rows <= 1:
+                return cols
+            if step >= cols:
+                return step
+    raise ValueError(f"{name} must be [rows, {cols}] with contiguous rows")
 
 
-def row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def empty(x: torch.Tensor, rows: int, cols: int, dtype: torch.dtype) -> torch.Tensor:
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=x.device)
 
 
-_NOTHING = contextlib.nullcontext()
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
 
 
 def on(x: torch.Tensor, stream):
-    """(context, stream pointer) to run on x's device: inside the context that device is current and, where a stream
-    was given, so is that stream, so that tensors allocated there belong to it."""
+    """(context, stream pointer) to run on x's device: inside the context (None: nothing to enter) that device is
+    current and, where a stream was given, so is that stream, so that tensors allocated there belong to it."""
     if stream is None:
-        ptr = torch.cuda.current_stream(x.device).cuda_stream
-        return (_NOTHING if x.device.index == torch.cuda.current_device() else torch.cuda.device(x.device)), ptr
+        at = x.get_device()
+        return (None if at == _current_device() else torch.cuda.device(at)), _raw_stream(at)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=x.device)
-    need(stream.device == x.device, f"the stream is on {stream.device}, the tensors on {x.device}")
+    if stream.device != x.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {x.device}")
     return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def run(x: torch.Tensor, stream, call, *args):
+    """call(stream pointer, *args) as `on` says."""
+    context, pointer = on(x, stream)
+    if context is None:
+        return call(pointer, *args)
+    with context:
+        return call(pointer, *args)

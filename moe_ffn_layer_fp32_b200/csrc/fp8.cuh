@@ -15,6 +15,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "mmoe.h"
 #include "sm100_async.cuh"
 #include "sm100_tc.cuh"
@@ -224,6 +226,15 @@ __device__ __forceinline__ float peer_load(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ float4 peer_load4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 // A bounded mbarrier wait.  Gives up after kWaitClk, or once another thread of the CTA has given up;
 // then it sets the CTA's abort word and the host-visible flag and returns false.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort_word, int* err, int site) {
@@ -331,6 +342,23 @@ __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) {
     const long long t0 = async::clk();
     while (!async::mbar_try_wait(bar, parity))
         if (async::clk() - t0 > kWaitClk) return;
+}
+
+// Lets a kernel have as much dynamic shared memory as a CTA can (asked for once a device: the call is not free).
+template <auto kKernel>
+cudaError_t allow_smem() {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (done.load(std::memory_order_acquire) >> dev & 1)) return e;
+    cudaFuncAttributes a;
+    int most = 0;
+    e = cudaFuncGetAttributes(&a, kKernel);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)a.sharedSizeBytes);
+    if (e == cudaSuccess) done.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+    return e;
 }
 
 // --- launchers ----------------------------------------------------------------

@@ -697,15 +697,38 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
         __syncwarp();
         cluster_arrive();
         cluster_wait();
-        if (warp >= 2) {
-            const int row = (warp & 3) * 32 + lane;
-            T* y = static_cast<T*>(p.y) + nt * kBlk + row;
-            for (int t = rank; t < m; t += C) {
-                float sum = 0.0f;
-#pragma unroll 4
-                for (int c = 0; c < C; ++c)
-                    sum += peer_load(peer_addr(reinterpret_cast<const float*>(sm->b) + t * kBlk + row, (uint32_t)c));
-                if (nt * kBlk + row < p.N && !sm->abort) y[t * p.ldy] = (T)sum;
+        if (warp >= 2 && !sm->abort) {
+            // every C-th row is this CTA's: a warp a row, two rows and all the peers' sums in flight
+            const int c4 = lane * 4, col = nt * kBlk + c4;
+            for (int i0 = warp - 2; rank + C * i0 < m; i0 += 8) {
+                float4 v[2][8];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int t = rank + C * (i0 + 4 * u);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        if (c < C && t < m)
+                            v[u][c] = peer_load4(peer_addr(reinterpret_cast<const float*>(sm->b) + t * kBlk + c4, (uint32_t)c));
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int t = rank + C * (i0 + 4 * u);
+                    if (t >= m) continue;
+                    float4 sum = v[u][0];
+#pragma unroll
+                    for (int c = 1; c < 8; ++c)
+                        if (c < C) {
+                            sum.x += v[u][c].x;
+                            sum.y += v[u][c].y;
+                            sum.z += v[u][c].z;
+                            sum.w += v[u][c].w;
+                        }
+                    T* y = static_cast<T*>(p.y) + t * p.ldy + col;
+                    if (col < p.N) y[0] = (T)sum.x;
+                    if (col + 1 < p.N) y[1] = (T)sum.y;
+                    if (col + 2 < p.N) y[2] = (T)sum.z;
+                    if (col + 3 < p.N) y[3] = (T)sum.w;
+                }
             }
         }
         // the partial sums stay until every CTA has read them
@@ -719,9 +742,9 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
     if (warp == 1) tc5::tmem_dealloc(tmem, kCols);
 }
 
-template <class K, class... A>
-cudaError_t launch(K kern, unsigned grid, unsigned threads, size_t smem, int cluster, cudaStream_t st, A... args) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <auto kKernel, class... A>
+cudaError_t launch(unsigned grid, unsigned threads, size_t smem, int cluster, cudaStream_t st, A... args) {
+    const cudaError_t e = allow_smem<kKernel>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -737,7 +760,7 @@ cudaError_t launch(K kern, unsigned grid, unsigned threads, size_t smem, int clu
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
+    return cudaLaunchKernelEx(&cfg, kKernel, args...);
 }
 
 template <bool kPair>
@@ -753,16 +776,16 @@ cudaError_t launch_many(const Product& p, const CUtensorMap& am, const CUtensorM
     constexpr int C = kPair ? 2 : 1;
     const unsigned grid = (unsigned)std::min<int64_t>(tiles, sm_count() / C) * C;
     const size_t smem = sizeof(Smem) + 1024;
-    return p.y_bf16 ? launch(product_kernel<kPair, __nv_bfloat16>, grid, kThreads, smem, C, st, am, wm, ym, wide, p)
-                    : launch(product_kernel<kPair, float>, grid, kThreads, smem, C, st, am, wm, ym, wide, p);
+    return p.y_bf16 ? launch<product_kernel<kPair, __nv_bfloat16>>(grid, kThreads, smem, C, st, am, wm, ym, wide, p)
+                    : launch<product_kernel<kPair, float>>(grid, kThreads, smem, C, st, am, wm, ym, wide, p);
 }
 
 template <int NT>
 cudaError_t launch_few(const Product& p, const CUtensorMap& wm, int C, cudaStream_t st) {
     const unsigned grid = (unsigned)(blocks_of(p.N) * C);
     const size_t smem = sizeof(SmallSmem<NT>) + 1024;
-    return p.y_bf16 ? launch(product_small_kernel<NT, __nv_bfloat16>, grid, kSThreads, smem, C, st, wm, p, C)
-                    : launch(product_small_kernel<NT, float>, grid, kSThreads, smem, C, st, wm, p, C);
+    return p.y_bf16 ? launch<product_small_kernel<NT, __nv_bfloat16>>(grid, kSThreads, smem, C, st, wm, p, C)
+                    : launch<product_small_kernel<NT, float>>(grid, kSThreads, smem, C, st, wm, p, C);
 }
 
 }  // namespace

@@ -198,15 +198,6 @@ struct ExpertShared {
     int last[kN];
 };
 
-__device__ __forceinline__ float4 peer_load4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
 __device__ __forceinline__ void peer_store8(uint32_t addr, uint2 v) {
     asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
 }
@@ -727,8 +718,7 @@ cudaError_t launch_experts(const MoePlan& p, int clusters, cudaStream_t st) {
     if (e == cudaSuccess) e = gate_up_map(&m[2], p.sh_gate_up, p.d, p.hs, 1, l.nu[1]);
     if (e == cudaSuccess) e = down_map(&m[3], p.sh_down, p.d, p.hs, 1, l.no);
     if (e != cudaSuccess) return e;
-    auto kern = moe_experts_kernel<S>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, l.bytes + 1024);
+    e = allow_smem<moe_experts_kernel<S>>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * S));
@@ -744,7 +734,7 @@ cudaError_t launch_experts(const MoePlan& p, int clusters, cudaStream_t st) {
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], p, l);
+    return cudaLaunchKernelEx(&cfg, moe_experts_kernel<S>, m[0], m[1], m[2], m[3], p, l);
 }
 
 }  // namespace
@@ -772,7 +762,7 @@ size_t carve_moe(MoePlan& p, unsigned char* base) {
 cudaError_t launch_moe_few(const MoePlan& p, cudaStream_t st) {
     const int ks = 32 * ((p.d / 32 + kRouteCluster - 1) / kRouteCluster);
     const size_t smem = (size_t)kRouteCluster * ks * 4;
-    cudaError_t e = cudaFuncSetAttribute(moe_route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem<moe_route_kernel>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((p.T + kRouteCluster - 1) / kRouteCluster * kRouteCluster));

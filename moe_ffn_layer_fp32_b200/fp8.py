@@ -13,7 +13,7 @@ import torch
 
 from . import _lib
 from ._lib import check, lib
-from ._tensors import E4M3, TYPE, blocks, need, on, row_stride, rows_of, same_device
+from ._tensors import E4M3, TYPE, blocks, empty, need, rows_of, run, same_device
 
 
 def _typed(t: torch.Tensor, name: str) -> int:
@@ -21,22 +21,25 @@ def _typed(t: torch.Tensor, name: str) -> int:
     return TYPE[t.dtype]
 
 
-def _scales(s: torch.Tensor, shape, name: str) -> None:
-    need(s.dtype == torch.float32 and tuple(s.shape) == tuple(shape) and s.is_contiguous(),
-         f"{name} must be contiguous float32 of shape {tuple(shape)}")
+def _scales(s: torch.Tensor, shape: tuple, name: str) -> None:
+    if s.dtype != torch.float32 or s.shape != shape or not s.is_contiguous():
+        raise ValueError(f"{name} must be contiguous float32 of shape {shape}")
 
 
 def _codes(q: torch.Tensor, dim: int, name: str) -> None:
-    need(q.dtype == E4M3 and q.dim() == dim and q.is_contiguous(), f"{name} must be a contiguous {dim}-D float8_e4m3fn tensor")
+    if q.dtype != E4M3 or q.dim() != dim or not q.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dim}-D float8_e4m3fn tensor")
 
 
 def _output(y, M: int, N: int, out_dtype, x: torch.Tensor):
+    """y, its type and the elements between its rows."""
     if y is None:
-        need(out_dtype in TYPE, "out_dtype must be float32 or bfloat16")
-        return torch.empty((M, N), dtype=out_dtype, device=x.device)
-    need(y.dtype in TYPE and y.shape[0] == M, f"y must be a float32 or bfloat16 tensor of {M} rows")
-    rows_of(y, N, "y")
-    return y
+        if out_dtype not in TYPE:
+            raise ValueError("out_dtype must be float32 or bfloat16")
+        return empty(x, M, N, out_dtype), TYPE[out_dtype], N
+    if y.dtype not in TYPE or y.shape[0] != M:
+        raise ValueError(f"y must be a float32 or bfloat16 tensor of {M} rows")
+    return y, TYPE[y.dtype], rows_of(y, N, "y")
 
 
 def quantize_fp8_rows(x: torch.Tensor, *, stream=None):
@@ -44,15 +47,15 @@ def quantize_fp8_rows(x: torch.Tensor, *, stream=None):
     [rows, ceil(K / 128)])."""
     need(x.dim() == 2, "x must be 2-D")
     M, K = x.shape
-    rows_of(x, K, "x")
-    kind = _typed(x, "x")
+    ldx, kind = rows_of(x, K, "x"), _typed(x, "x")
     same_device(x)
-    ctx, st = on(x, stream)
-    with ctx:
-        q = torch.empty((M, K), dtype=E4M3, device=x.device)
-        s = torch.empty((M, blocks(K)), dtype=torch.float32, device=x.device)
-        check(lib().mmoe_quantize_fp8_rows(x.data_ptr(), kind, M, K, row_stride(x), q.data_ptr(), s.data_ptr(), st))
-    return q, s
+
+    def call(st):
+        q, s = empty(x, M, K, E4M3), empty(x, M, blocks(K), torch.float32)
+        check(lib().mmoe_quantize_fp8_rows(x.data_ptr(), kind, M, K, ldx, q.data_ptr(), s.data_ptr(), st))
+        return q, s
+
+    return run(x, stream, call)
 
 
 def quantize_fp8_blocks(w: torch.Tensor, *, stream=None):
@@ -63,12 +66,14 @@ def quantize_fp8_blocks(w: torch.Tensor, *, stream=None):
     same_device(w)
     N, K = w.shape[-2:]
     batch = w.shape[:-2].numel()
-    ctx, st = on(w, stream)
-    with ctx:
+
+    def call(st):
         q = torch.empty(w.shape, dtype=E4M3, device=w.device)
         s = torch.empty((*w.shape[:-2], blocks(N), blocks(K)), dtype=torch.float32, device=w.device)
         check(lib().mmoe_quantize_fp8_blocks(w.data_ptr(), kind, batch, N, K, q.data_ptr(), s.data_ptr(), st))
-    return q, s
+        return q, s
+
+    return run(w, stream, call)
 
 
 def gemm_fp8(xq: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor, y: torch.Tensor | None = None, *,
@@ -77,16 +82,18 @@ def gemm_fp8(xq: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: torch.Ten
     (float32 or bfloat16, rows contiguous)."""
     _codes(xq, 2, "xq")
     _codes(wq, 2, "wq")
-    (M, K), N = xq.shape, wq.shape[0]
-    need(wq.shape[1] == K, "xq and wq must have the same K")
+    (M, K), (N, Kw) = xq.shape, wq.shape
+    if Kw != K:
+        raise ValueError("xq and wq must have the same K")
     _scales(sx, (M, blocks(K)), "sx")
     _scales(sw, (blocks(N), blocks(K)), "sw")
     same_device(xq, sx, wq, sw, y)
-    ctx, st = on(xq, stream)
-    with ctx:
-        y = _output(y, M, N, out_dtype, xq)
-        check(lib().mmoe_gemm_fp8(xq.data_ptr(), sx.data_ptr(), M, wq.data_ptr(), sw.data_ptr(), N, K, y.data_ptr(),
-                                  TYPE[y.dtype], row_stride(y), st))
+    return run(xq, stream, _gemm, xq, sx, wq, sw, y, out_dtype, M, N, K)
+
+
+def _gemm(st, xq, sx, wq, sw, y, out_dtype, M, N, K):
+    y, kind, ldy = _output(y, M, N, out_dtype, xq)
+    check(lib().mmoe_gemm_fp8(xq.data_ptr(), sx.data_ptr(), M, wq.data_ptr(), sw.data_ptr(), N, K, y.data_ptr(), kind, ldy, st))
     return y
 
 
@@ -97,18 +104,21 @@ def grouped_gemm_fp8(xq: torch.Tensor, sx: torch.Tensor, offsets: torch.Tensor, 
     the device.  Rows outside [offsets[0], offsets[G]) of a given y stay as they were (of a new one: undefined)."""
     _codes(xq, 2, "xq")
     _codes(wq, 3, "wq")
-    (M, K), (G, N) = xq.shape, wq.shape[:2]
-    need(wq.shape[2] == K, "xq and wq must have the same K")
+    (M, K), (G, N, Kw) = xq.shape, wq.shape
+    if Kw != K:
+        raise ValueError("xq and wq must have the same K")
     _scales(sx, (M, blocks(K)), "sx")
     _scales(sw, (G, blocks(N), blocks(K)), "sw")
-    need(offsets.dtype == torch.int32 and offsets.shape == (G + 1,) and offsets.is_contiguous(),
-         f"offsets must be contiguous int32 of shape ({G + 1},)")
+    if offsets.dtype != torch.int32 or offsets.shape != (G + 1,) or not offsets.is_contiguous():
+        raise ValueError(f"offsets must be contiguous int32 of shape ({G + 1},)")
     same_device(xq, sx, wq, sw, offsets, y)
-    ctx, st = on(xq, stream)
-    with ctx:
-        y = _output(y, M, N, out_dtype, xq)
-        check(lib().mmoe_gemm_fp8_grouped(xq.data_ptr(), sx.data_ptr(), M, offsets.data_ptr(), G, wq.data_ptr(),
-                                          sw.data_ptr(), N, K, y.data_ptr(), TYPE[y.dtype], row_stride(y), st))
+    return run(xq, stream, _grouped, xq, sx, offsets, wq, sw, y, out_dtype, M, G, N, K)
+
+
+def _grouped(st, xq, sx, offsets, wq, sw, y, out_dtype, M, G, N, K):
+    y, kind, ldy = _output(y, M, N, out_dtype, xq)
+    check(lib().mmoe_gemm_fp8_grouped(xq.data_ptr(), sx.data_ptr(), M, offsets.data_ptr(), G, wq.data_ptr(), sw.data_ptr(),
+                                      N, K, y.data_ptr(), kind, ldy, st))
     return y
 
 
@@ -117,31 +127,34 @@ def linear_fp8(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor, y: torch.Ten
     """quantize_fp8_rows of x [M, K] (bfloat16, rows contiguous), then gemm_fp8: y [M, N].  Up to 64 rows are one
     launch."""
     _codes(wq, 2, "wq")
-    need(x.dtype == torch.bfloat16 and x.dim() == 2, "x must be a 2-D bfloat16 tensor")
-    (M, K), N = x.shape, wq.shape[0]
-    need(wq.shape[1] == K, "x and wq must have the same K")
-    rows_of(x, K, "x")
+    if x.dtype != torch.bfloat16 or x.dim() != 2:
+        raise ValueError("x must be a 2-D bfloat16 tensor")
+    (M, K), (N, Kw) = x.shape, wq.shape
+    if Kw != K:
+        raise ValueError("x and wq must have the same K")
+    ldx = rows_of(x, K, "x")
     _scales(sw, (blocks(N), blocks(K)), "sw")
     same_device(x, wq, sw, y)
-    ctx, st = on(x, stream)
-    with ctx:
-        y = _output(y, M, N, out_dtype, x)
-        size, room, at = 0, None, None
-        if M > 64:
-            bytes_ = C.c_size_t()
-            check(lib().mmoe_linear_fp8_workspace(M, K, C.byref(bytes_)))
-            size = bytes_.value
-            room = torch.empty(size, dtype=torch.uint8, device=x.device)
-            at = room.data_ptr()
-        check(lib().mmoe_linear_fp8(x.data_ptr(), M, row_stride(x), wq.data_ptr(), sw.data_ptr(), N, K, y.data_ptr(),
-                                    TYPE[y.dtype], row_stride(y), at, size, st))
+    return run(x, stream, _linear, x, ldx, wq, sw, y, out_dtype, M, N, K)
+
+
+def _linear(st, x, ldx, wq, sw, y, out_dtype, M, N, K):
+    y, kind, ldy = _output(y, M, N, out_dtype, x)
+    size, room, at = 0, None, None
+    if M > 64:
+        size = 16 * -(-M * blocks(K) // 4) + M * K  # mmoe_linear_fp8_workspace
+        room = empty(x, 1, size, torch.uint8)
+        at = room.data_ptr()
+    check(lib().mmoe_linear_fp8(x.data_ptr(), M, ldx, wq.data_ptr(), sw.data_ptr(), N, K, y.data_ptr(), kind, ldy, at, size,
+                                st))
     return y
 
 
-def _optional(t: torch.Tensor | None, shape, dtype, name: str):
+def _optional(t: torch.Tensor | None, shape: tuple, dtype, name: str):
     if t is None:
         return None
-    need(t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous(), f"{name} must be contiguous {dtype} of shape {shape}")
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} of shape {shape}")
     return t.data_ptr()
 
 
@@ -156,6 +169,8 @@ class FP8MoELayer:
         self.cfg = _lib.Config(d_model, n_experts, top_k, expert_hidden,
                                expert_hidden if shared_hidden is None else shared_hidden, 128, max_tokens, gating,
                                int(has_router_bias), 0)
+        self._sizes = d_model, top_k, n_experts
+        self._config = C.byref(self.cfg)
         self._keep = None
         self._room: dict[int, int] = {}  # workspace bytes for a number of tokens
         self._workspace_bytes(0)         # checks the config
@@ -192,31 +207,36 @@ class FP8MoELayer:
         same_device(*keep)
         self._keep = keep
         self._weights = _lib.FP8Weights(*[None if t is None else t.data_ptr() for t in keep])
+        self._pointers = C.byref(self._weights)
 
     def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, *, out_dtype: torch.dtype = torch.float32, stream=None,
                 topk_idx=None, topk_gate=None, expert_counts=None) -> torch.Tensor:
         """y [T, d] (given, or new of out_dtype: float32 or bfloat16) from x [T, d] (bfloat16, contiguous)."""
-        c = self.cfg
-        d, k = c.d_model, c.top_k
-        need(self._keep is not None, "the layer has no weights: call load() first")
-        need(x.dtype == torch.bfloat16 and x.dim() == 2 and x.shape[1] == d and x.is_contiguous(),
-             "x must be a contiguous [T, d_model] bfloat16 tensor")
+        if self._keep is None:
+            raise ValueError("the layer has no weights: call load() first")
+        d, k, E = self._sizes
+        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != d or not x.is_contiguous():
+            raise ValueError("x must be a contiguous [T, d_model] bfloat16 tensor")
         T = x.shape[0]
-        out = (_optional(topk_idx, (T, k), torch.int32, "topk_idx"), _optional(topk_gate, (T, k), torch.float32, "topk_gate"),
-               _optional(expert_counts, (c.n_experts + 1,), torch.int32, "expert_counts"))
+        idx, gate = _optional(topk_idx, (T, k), torch.int32, "topk_idx"), _optional(topk_gate, (T, k), torch.float32, "topk_gate")
+        counts = _optional(expert_counts, (E + 1,), torch.int32, "expert_counts")
         same_device(x, self._keep[0], y, topk_idx, topk_gate, expert_counts)
-        room = self._workspace_bytes(T)
-        ctx, st = on(x, stream)
-        with ctx:
-            if y is None:
-                need(out_dtype in TYPE, "out_dtype must be float32 or bfloat16")
-                y = torch.empty((T, d), dtype=out_dtype, device=x.device)
-            else:
-                need(y.dtype in TYPE and tuple(y.shape) == (T, d) and y.is_contiguous(),
-                     "y must be a contiguous [T, d_model] float32 or bfloat16 tensor")
-            space = torch.empty(room, dtype=torch.uint8, device=x.device)
-            check(lib().mmoe_forward_fp8(C.byref(c), C.byref(self._weights), x.data_ptr(), T, y.data_ptr(), TYPE[y.dtype],
-                                         *out, space.data_ptr(), room, st))
+        return run(x, stream, self._forward, x, T, y, out_dtype, idx, gate, counts)
+
+    def _forward(self, st, x, T, y, out_dtype, idx, gate, counts):
+        d = self._sizes[0]
+        if y is None:
+            if out_dtype not in TYPE:
+                raise ValueError("out_dtype must be float32 or bfloat16")
+            y = empty(x, T, d, out_dtype)
+        elif y.dtype not in TYPE or y.shape != (T, d) or not y.is_contiguous():
+            raise ValueError("y must be a contiguous [T, d_model] float32 or bfloat16 tensor")
+        size = self._room.get(T)
+        if size is None:
+            size = self._workspace_bytes(T)
+        room = empty(x, 1, size, torch.uint8)
+        check(lib().mmoe_forward_fp8(self._config, self._pointers, x.data_ptr(), T, y.data_ptr(), TYPE[y.dtype], idx, gate,
+                                     counts, room.data_ptr(), size, st))
         return y
 
     __call__ = forward

@@ -7,13 +7,14 @@ import torch
 
 from . import _lib
 from ._lib import check, lib
-from ._tensors import E4M3, TYPE, blocks, need, on, row_stride, rows_of, same_device
+from ._tensors import E4M3, TYPE, blocks, empty, need, rows_of, run, same_device
 
 
 def _weight(w: torch.Tensor | None, d: int, name: str):
     if w is None:
         return None
-    need(w.dtype == torch.float32 and w.shape == (d,) and w.is_contiguous(), f"{name} must be contiguous float32 of shape ({d},)")
+    if w.dtype != torch.float32 or w.shape != (d,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be contiguous float32 of shape ({d},)")
     return w.data_ptr()
 
 
@@ -22,11 +23,13 @@ def _gate(gate: torch.Tensor | None, T: int, d: int):
     if gate is None:
         return None, 0, 0
     need(gate.dtype == torch.float32, "gate must be float32")
-    if gate.dim() == 1:
-        gate = gate.unsqueeze(0)
-    need(gate.dim() == 2 and gate.shape[0] in (1, T) and gate.shape[1] in (1, d), f"gate must be [{d}], [{T}, 1], [1, {d}] or [{T}, {d}]")
-    row = gate.stride(0) if gate.shape[0] > 1 else 0
-    col = gate.stride(1) if gate.shape[1] > 1 else 0
+    shape, step = tuple(gate.shape), gate.stride()
+    if len(shape) == 1:
+        shape, step = (1, *shape), (0, *step)
+    if len(shape) != 2 or shape[0] not in (1, T) or shape[1] not in (1, d):
+        raise ValueError(f"gate must be [{d}], [{T}, 1], [1, {d}] or [{T}, {d}]")
+    row = step[0] if shape[0] > 1 else 0
+    col = step[1] if shape[1] > 1 else 0
     need(col in (0, 1), "gate must have contiguous rows")
     return gate.data_ptr(), row, col
 
@@ -43,36 +46,40 @@ def block_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *, post_we
     xq, sx are x's e4m3 codes and scales per 128 features (None without quantize).  Without y, r' is the scaled
     residual, and None unless out_residual is given.  r' goes into out_residual (which may be ``residual`` itself) or a
     new tensor.  Nothing is rounded before the outputs."""
-    need(residual.dim() == 2 and residual.dtype in TYPE, "residual must be a 2-D float32 or bfloat16 tensor")
+    if residual.dim() != 2 or residual.dtype not in TYPE:
+        raise ValueError("residual must be a 2-D float32 or bfloat16 tensor")
     T, d = residual.shape
-    rows_of(residual, d, "residual")
+    ldr = rows_of(residual, d, "residual")
+    kind, y_kind, y_at, ldy = TYPE[residual.dtype], _lib.F32, None, 0
     if y is not None:
-        need(y.dtype in TYPE and y.dim() == 2 and y.shape[0] == T, f"y must be a float32 or bfloat16 tensor of {T} rows")
-        rows_of(y, d, "y")
+        if y.dtype not in TYPE or y.dim() != 2 or y.shape[0] != T:
+            raise ValueError(f"y must be a float32 or bfloat16 tensor of {T} rows")
+        y_kind, y_at, ldy = TYPE[y.dtype], y.data_ptr(), rows_of(y, d, "y")
+    out_at, ldo = None, 0
     if out_residual is not None:
-        need(out_residual.dtype == residual.dtype and out_residual.dim() == 2 and out_residual.shape[0] == T,
-             "out_residual must have residual's type and rows")
-        rows_of(out_residual, d, "out_residual")
+        if out_residual.dtype != residual.dtype or out_residual.dim() != 2 or out_residual.shape[0] != T:
+            raise ValueError("out_residual must have residual's type and rows")
+        out_at, ldo = out_residual.data_ptr(), rows_of(out_residual, d, "out_residual")
     need(not quantize or pre_weight is not None, "quantize needs pre_weight")
     post, pre = _weight(post_weight, d, "post_weight"), _weight(pre_weight, d, "pre_weight")
-    gp, gr, gc = _gate(gate, T, d)
+    gate_at, gate_row, gate_col = _gate(gate, T, d)
     same_device(residual, y, post_weight, gate, pre_weight, out_residual)
-    ctx, st = on(residual, stream)
-    dev = residual.device
-    with ctx:
-        if out_residual is None and y is not None:
-            out_residual = torch.empty((T, d), dtype=residual.dtype, device=dev)
-        x = xq = sx = None
+
+    def call(st):
+        out, o_at, o_ld = out_residual, out_at, ldo
+        if out is None and y is not None:
+            out = empty(residual, T, d, residual.dtype)
+            o_at, o_ld = out.data_ptr(), d
+        x = xq = sx = x_at = xq_at = sx_at = None
         if pre is not None:
-            x = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
+            x = empty(residual, T, d, torch.bfloat16)
+            x_at = x.data_ptr()
             if quantize:
-                xq = torch.empty((T, d), dtype=E4M3, device=dev)
-                sx = torch.empty((T, blocks(d)), dtype=torch.float32, device=dev)
-        n = _lib.Norm(T, d, TYPE[residual.dtype], _lib.F32 if y is None else TYPE[y.dtype], gc, gr, residual_scale, eps,
-                      residual.data_ptr(), row_stride(residual), None if y is None else y.data_ptr(),
-                      0 if y is None else row_stride(y), post, gp, pre,
-                      None if out_residual is None else out_residual.data_ptr(),
-                      0 if out_residual is None else row_stride(out_residual), None if x is None else x.data_ptr(),
-                      None if xq is None else xq.data_ptr(), None if sx is None else sx.data_ptr())
+                xq, sx = empty(residual, T, d, E4M3), empty(residual, T, blocks(d), torch.float32)
+                xq_at, sx_at = xq.data_ptr(), sx.data_ptr()
+        n = _lib.Norm(T, d, kind, y_kind, gate_col, gate_row, residual_scale, eps, residual.data_ptr(), ldr, y_at, ldy, post,
+                      gate_at, pre, o_at, o_ld, x_at, xq_at, sx_at)
         check(lib().mmoe_block_norm(C.byref(n), st))
-    return out_residual, x, xq, sx
+        return out, x, xq, sx
+
+    return run(residual, stream, call)
