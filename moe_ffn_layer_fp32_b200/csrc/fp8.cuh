@@ -40,7 +40,14 @@ __device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.laun
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-__device__ __forceinline__ float scale_of(uint32_t amax_bits) { return __fdiv_rn(__uint_as_float(amax_bits), kTop); }
+// max|v| / 448, the IEEE quotient.  Division by a constant after Brisebarre, Muller and Raina ("Accelerating correctly
+// rounded floating-point division when the divisor is known in advance"): the product with the rounded reciprocal and
+// one correction by its remainder.  Checked over every significand; below 2^-100, for infinities and NaN it divides.
+__device__ __forceinline__ float scale_of(uint32_t amax_bits) {
+    const float a = __uint_as_float(amax_bits), q = a * (1.0f / kTop);
+    const float s = fmaf(fmaf(-kTop, q, a), 1.0f / kTop, q);
+    return a >= 0x1p-100f && a <= 3.0e38f ? s : __fdiv_rn(a, kTop);
+}
 
 __device__ __forceinline__ float coded(float v, float s) { return s > 0.0f ? __fdiv_rn(v, s) : 0.0f; }
 
@@ -53,35 +60,35 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) { return e4m3x2(a, b) | (e4m3x2(c, d) << 16); }
 
-// The codes of a block's values, e4m3(v / s), without a division for each.  hi and lo are 1 / s moved up and down by
-// 2^-21: rcp.approx is off by 2^-23 at most, each product rounds by 2^-24, so v * lo and v * hi lie on either side of
-// the FP32 quotient, and where they have the same code it is the quotient's.  Where they do not (a rounding border
-// within 2^-21, about one value in 10^5), or 1 / s is not a normal number (s zero, tiny, huge, NaN or infinite), the
-// values are divided.  Quantising 32768 x 2048 BF16 values took 106 us with the divisions, and takes 37 us.
-// The divisions are a call: inlined they are most of a kernel's code, and a kernel of a few microseconds waits for its code.
-static __device__ __noinline__ uint2 divided8(float a, float b, float c, float d, float e, float f, float g, float h, float s) {
-    return make_uint2(e4m3x4(coded(a, s), coded(b, s), coded(c, s), coded(d, s)),
-                      e4m3x4(coded(e, s), coded(f, s), coded(g, s), coded(h, s)));
+// A call: inlined, divisions would be most of a kernel's code, and a kernel of a few microseconds waits for its code.
+static __device__ __noinline__ uint32_t divided4(float a, float b, float c, float d, float s) {
+    return e4m3x4(coded(a, s), coded(b, s), coded(c, s), coded(d, s));
 }
 
+// The codes of a block's values, e4m3(v / s), from one reciprocal: y = RN(1 / s), a quotient v y and two corrections by
+// its remainder, q + (v - q s) y.  The first leaves q within an ulp of v / s, after which the second gives RN(v / s)
+// itself (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990), as long as no
+// remainder underflows: a code that is not 0 needs v >= s 2^-11, and the remainder is a multiple of v 2^-47.  Blocks
+// outside these limits, of zeros, with NaN or infinities are divided.  (Bounding the quotient from both sides by two
+// products is cheaper, but BF16 values lie on a rounding border too often: one in 200.)  Quantising 32768 x 2048 BF16
+// values took 106 us with a division each.
 struct Coder {
-    float s, hi, lo;
+    float s, y;
     bool fast;
     __device__ __forceinline__ explicit Coder(float scale) : s(scale) {
-        float r;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale));
-        fast = scale >= 0x1p-120f && scale <= 0x1p120f;
-        hi = r * (1.0f + 0x1p-21f);
-        lo = r * (1.0f - 0x1p-21f);
+        y = __fdiv_rn(1.0f, scale);
+        fast = scale >= 0x1p-80f && scale <= 0x1p100f;
+    }
+    __device__ __forceinline__ uint32_t pair(float a, float b) const {
+        const float2 v = make_float2(a, b), yy = make_float2(y, y), ms = make_float2(-s, -s);
+        float2 q = __fmul2_rn(v, yy);
+        q = __ffma2_rn(__ffma2_rn(ms, q, v), yy, q);
+        q = __ffma2_rn(__ffma2_rn(ms, q, v), yy, q);
+        return e4m3x2(q.x, q.y);
     }
     __device__ __forceinline__ uint2 operator()(const float (&v)[8]) const {
-        uint2 h, l;
-        h.x = e4m3x4(v[0] * hi, v[1] * hi, v[2] * hi, v[3] * hi);
-        h.y = e4m3x4(v[4] * hi, v[5] * hi, v[6] * hi, v[7] * hi);
-        l.x = e4m3x4(v[0] * lo, v[1] * lo, v[2] * lo, v[3] * lo);
-        l.y = e4m3x4(v[4] * lo, v[5] * lo, v[6] * lo, v[7] * lo);
-        if (!fast || h.x != l.x || h.y != l.y) h = divided8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], s);
-        return h;
+        if (!fast) return make_uint2(divided4(v[0], v[1], v[2], v[3], s), divided4(v[4], v[5], v[6], v[7], s));
+        return make_uint2(pair(v[0], v[1]) | pair(v[2], v[3]) << 16, pair(v[4], v[5]) | pair(v[6], v[7]) << 16);
     }
 };
 
@@ -117,6 +124,35 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t m) {
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
+}
+
+// Scales and codes of the first n of U blocks, 16 lanes (8 values each, get(u, values)) a block.  All of them side by
+// side: one after the other each waits for its own maximum, reciprocal and conversions.
+template <int U, class Get>
+__device__ __forceinline__ void encode(int n, const Get& get, float (&s)[U], uint2 (&q)[U]) {
+    uint32_t m[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        m[u] = 0;
+        if (u < n) {
+            float v[8];
+            get(u, v);
+            m[u] = amax8(v);
+        }
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (u < n) m[u] = max(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (u < n) {
+            float v[8];
+            get(u, v);
+            s[u] = scale_of(m[u]);
+            q[u] = Coder(s[u])(v);
+        }
 }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {

@@ -599,7 +599,7 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
             // operand rows of this round: a half warp per (row, block)
             const int n = min(kRound, mine - i0);
             const int hl = pt & 15;
-            constexpr int kBatch = NT / 8;  // in flight a half warp: every row of a block
+            constexpr int kBatch = NT == 16 ? 4 : 8;  // (row, block) items in flight a half warp
             const float inv = __fdividef(1.0f, (float)m);
             // (both half warps of a warp make the same turns: they meet in the shuffles)
             for (int jw = pt >> 5 << 1; jw < n * m; jw += 8 * kBatch) {
@@ -625,19 +625,19 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
                         sc[u] = p.sa[(int64_t)t * KB + kb];
                     }
                 }
+                uint2 code[kBatch];
+                if (p.x) {
+                    encode<kBatch>((n * m - jw + 7) / 8, [&](int u, float (&v)[8]) { unpack8(raw[u], v); }, sc, code);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) code[u] = make_uint2(raw[u].x, raw[u].y);
+                }
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
                     if (jw + 8 * u >= n * m) continue;
-                    uint2 code = make_uint2(raw[u].x, raw[u].y);
-                    if (p.x) {
-                        float v[8];
-                        unpack8(raw[u], v);
-                        sc[u] = scale_of(half_warp_max(amax8(v)));
-                        code = Coder(sc[u])(v);
-                    }
                     if (hl == 0) (&sm->sx[0][0])[at[u]] = sc[u];
                     // 128-byte swizzle: 16-byte chunk c of row t lies at chunk c ^ (t & 7) (NT is a multiple of 8)
-                    *reinterpret_cast<uint2*>(sm->b + at[u] * kBlk + (((hl >> 1) ^ (at[u] & 7)) << 4) + (hl & 1) * 8) = code;
+                    *reinterpret_cast<uint2*>(sm->b + at[u] * kBlk + (((hl >> 1) ^ (at[u] & 7)) << 4) + (hl & 1) * 8) = code[u];
                 }
             }
             fence_async_smem();

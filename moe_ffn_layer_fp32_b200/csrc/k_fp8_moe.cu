@@ -579,20 +579,23 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
                         b[u] = peer_load4(from + 16);
                     }
                 }
+                float scale[4];
+                uint2 code[4];
+                encode<4>((own - jw + 7) / 8, [&](int u, float (&v)[8]) {
+                    v[0] = a[u].x; v[1] = a[u].y; v[2] = a[u].z; v[3] = a[u].w;
+                    v[4] = b[u].x; v[5] = b[u].y; v[6] = b[u].z; v[7] = b[u].w;
+                }, scale, code);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     if (jw + 8 * u >= own) continue;
-                    const float v[8] = {a[u].x, a[u].y, a[u].z, a[u].w, b[u].x, b[u].y, b[u].z, b[u].w};
-                    const float s = scale_of(half_warp_max(amax8(v)));
-                    const uint2 code = Coder(s)(v);
                     uint8_t* to = operand + at[u] * kBlk + (((hl >> 1) ^ (at[u] & 7)) << 4) + (hl & 1) * 8;
                     if (stride == 1) {
-                        *reinterpret_cast<uint2*>(to) = code;
-                        if (hl == 0) sh[at[u]] = s;
+                        *reinterpret_cast<uint2*>(to) = code[u];
+                        if (hl == 0) sh[at[u]] = scale[u];
                     } else {
 #pragma unroll
-                        for (int r = 0; r < S; ++r) peer_store8(peer_addr(to, (uint32_t)r), code);
-                        if (hl < S) peer_store(peer_addr(sh + at[u], (uint32_t)hl), s);
+                        for (int r = 0; r < S; ++r) peer_store8(peer_addr(to, (uint32_t)r), code[u]);
+                        if (hl < S) peer_store(peer_addr(sh + at[u], (uint32_t)hl), scale[u]);
                     }
                 }
             }

@@ -38,13 +38,17 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const T* x, int
         for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
         if (b < nblk && col[i] < K) load8(x + row[i] * ldx + col[i], v[i]);
     }
+    float sc[kItems];
+    uint2 code[kItems];
+    encode<kItems>(kItems, [&](int i, float (&o)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = v[i][j];
+    }, sc, code);
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-        const float sc = scale_of(half_warp_max(amax8(v[i])));
         if (first + i >= nblk) continue;
-        if (hl == 0) s[first + i] = sc;
-        if (col[i] < K)
-            *reinterpret_cast<uint2*>(q + row[i] * K + col[i]) = Coder(sc)(v[i]);
+        if (hl == 0) s[first + i] = sc[i];
+        if (col[i] < K) *reinterpret_cast<uint2*>(q + row[i] * K + col[i]) = code[i];
     }
 }
 
