@@ -65,24 +65,26 @@ static __device__ __noinline__ uint32_t divided4(float a, float b, float c, floa
     return e4m3x4(coded(a, s), coded(b, s), coded(c, s), coded(d, s));
 }
 
-// The codes of a block's values, e4m3(v / s), from one reciprocal: y = RN(1 / s), a quotient v y and two corrections by
-// its remainder, q + (v - q s) y.  The first leaves q within an ulp of v / s, after which the second gives RN(v / s)
-// itself (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990), as long as no
-// remainder underflows: a code that is not 0 needs v >= s 2^-11, and the remainder is a multiple of v 2^-47.  Blocks
-// outside these limits, of zeros, with NaN or infinities are divided.  (Bounding the quotient from both sides by two
-// products is cheaper, but BF16 values lie on a rounding border too often: one in 200.)  Quantising 32768 x 2048 BF16
-// values took 106 us with a division each.
+// The codes of a block's values, e4m3(v / s), from one reciprocal: y = RN(1 / s), the quotient v y and one correction by
+// its remainder, RN(q + (v - q s) y).  Before that last rounding it is within 2^-46 of v / s, relative, so that it is the
+// IEEE quotient unless v / s lies 2^-22 of an ulp or less from the middle of two FP32 numbers.  That matters for the code
+// only beside a rounding border of e4m3, a number of four significant bits; with significands V, S < 2^24 the middle beside
+// it, B 2^20 + 1 with B below 2^5, can be as near to V / S only where S is within 4 of a multiple of 2^20.  For those S
+// (16 either way) every V was checked on the CPU: always the IEEE quotient.  A code that is not 0 needs v >= s 2^-11, and
+// the remainder is a multiple of v 2^-47, which must not underflow; blocks outside that range, of zeros, with NaN or
+// infinities are divided.  (Bounding the quotient from both sides by two products costs less, but BF16 values lie on a
+// border too often: one in 200.)  Quantising 32768 x 2048 BF16 values took 106 us with a division each, and takes 45 us.
 struct Coder {
     float s, y;
     bool fast;
-    __device__ __forceinline__ explicit Coder(float scale) : s(scale) {
-        y = __fdiv_rn(1.0f, scale);
+    __device__ __forceinline__ explicit Coder(float scale) : Coder(scale, inverse(scale)) {}
+    static __device__ __forceinline__ float inverse(float scale) { return __fdiv_rn(1.0f, scale); }
+    __device__ __forceinline__ Coder(float scale, float inv) : s(scale), y(inv) {
         fast = scale >= 0x1p-80f && scale <= 0x1p100f;
     }
     __device__ __forceinline__ uint32_t pair(float a, float b) const {
         const float2 v = make_float2(a, b), yy = make_float2(y, y), ms = make_float2(-s, -s);
         float2 q = __fmul2_rn(v, yy);
-        q = __ffma2_rn(__ffma2_rn(ms, q, v), yy, q);
         q = __ffma2_rn(__ffma2_rn(ms, q, v), yy, q);
         return e4m3x2(q.x, q.y);
     }
@@ -126,32 +128,38 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t m) {
     return m;
 }
 
-// Scales and codes of the first n of U blocks, 16 lanes (8 values each, get(u, values)) a block.  All of them side by
-// side: one after the other each waits for its own maximum, reciprocal and conversions.
-template <int U, class Get>
-__device__ __forceinline__ void encode(int n, const Get& get, float (&s)[U], uint2 (&q)[U]) {
+// Largest magnitude of 8 BF16 values, as FP32 bits.
+__device__ __forceinline__ uint32_t amax_bf16(const uint4& u) {
+    const uint32_t k = 0x7fff7fffu;
+    const uint32_t m = __vmaxu2(__vmaxu2(u.x & k, u.y & k), __vmaxu2(u.z & k, u.w & k));
+    return max(m << 16, m & 0xffff0000u);
+}
+
+// Scales and codes of the first n of U blocks, 16 lanes (8 values each) a block: peak(u) gives a lane's largest
+// magnitude, get(u, values) the values.  All blocks side by side, for one after the other each waits for its own
+// maximum, divisions and conversions; lane u of the 16 does block u's divisions.
+template <int U, class Peak, class Get>
+__device__ __forceinline__ void encode(int n, const Peak& peak, const Get& get, float (&s)[U], uint2 (&q)[U]) {
     uint32_t m[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        m[u] = 0;
-        if (u < n) {
-            float v[8];
-            get(u, v);
-            m[u] = amax8(v);
-        }
-    }
+    for (int u = 0; u < U; ++u) m[u] = u < n ? peak(u) : 0u;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1)
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (u < n) m[u] = max(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
+    uint32_t mine = m[0];
+#pragma unroll
+    for (int u = 1; u < U; ++u)
+        if ((threadIdx.x & (U - 1)) == u) mine = m[u];
+    const float scale = scale_of(mine), inv = Coder::inverse(scale);
 #pragma unroll
     for (int u = 0; u < U; ++u)
         if (u < n) {
             float v[8];
             get(u, v);
-            s[u] = scale_of(m[u]);
-            q[u] = Coder(s[u])(v);
+            s[u] = __shfl_sync(0xffffffffu, scale, u, 16);
+            q[u] = Coder(s[u], __shfl_sync(0xffffffffu, inv, u, 16))(v);
         }
 }
 

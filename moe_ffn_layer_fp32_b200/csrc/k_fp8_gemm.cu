@@ -94,7 +94,6 @@ constexpr int kTileBytes = kBlk * kBlk;  // one 128 x 128 operand tile: 16 KB
 constexpr int kTmemCols = 512;            // two or four buffers of a tile's width
 constexpr int kMaxBufs = 4;
 constexpr int kTInfo = 4;                // tiles published ahead
-constexpr int kIssuers = 2;
 constexpr int kPromoWarps = 8;
 constexpr int kThreads = 128 + 32 * kPromoWarps;
 // Register split (setmaxnreg): 168 a thread at launch; warpgroup 0 drops to 40, the promotion rises to 232.
@@ -110,10 +109,13 @@ struct TileInfo {
     int64_t row0;
 };
 
-constexpr int kStages = 4;
-
+// A tile is C x 128 rows and H x 128 columns, by a pair of CTAs (C = 2, each with 128 rows, and with half of the weight
+// rows in its shared memory) or by one.
+template <int C, int H>
 struct Smem {
-    alignas(1024) uint8_t ring[kStages][2 * kTileBytes];  // 128 activation rows, 128 weight rows
+    static constexpr int kWeights = H / C * kTileBytes;            // of a block of K, in a CTA
+    static constexpr int kStages = H > C ? 3 : 4;
+    alignas(1024) uint8_t ring[kStages][kTileBytes + kWeights];    // 128 activation rows, the weight rows
     alignas(1024) uint8_t out[kPromoWarps][kOutBytes];
     uint64_t full[kStages], empty[kStages];
     uint64_t accf[kMaxBufs], acce[kMaxBufs];
@@ -127,8 +129,9 @@ struct Smem {
 
 // Offsets of the groups, made harmless: within [0, M] and not decreasing, whatever the array holds.
 // Warp 0 of the CTA; 32 groups a step.
-template <int kRows>
-__device__ __forceinline__ void load_groups(const Product& p, Smem* sm, int lane) {
+template <int C, int H>
+__device__ __forceinline__ void load_groups(const Product& p, Smem<C, H>* sm, int lane) {
+    constexpr int kRows = C * kBlk;
     int prev = 0, base = 0;
     for (int g0 = 0; g0 < p.groups; g0 += 32) {
         const int g = g0 + lane;
@@ -183,9 +186,20 @@ __device__ __forceinline__ void stage_row(uint8_t* box, int r, const float2* acc
 }
 
 // ... and where the copy engine may not write it (rows behind the tile's that belong to another group, rows of y that
-// are not whole 16 bytes) the warp does, element by element.
+// are not whole 16 bytes) the warp does: 16 bytes a lane, or element by element.
 template <class T>
-__device__ __forceinline__ void store_box(const uint8_t* box, T* y, int64_t ldy, int nr, int col, int N, int lane) {
+__device__ __forceinline__ void store_box(const uint8_t* box, T* y, int64_t ldy, int nr, int col, int N, bool wide, int lane) {
+    if (wide) {  // N is whole 16 bytes too
+        const int c = lane & 7, at = col + c * (16 / (int)sizeof(T));
+        if (at >= N) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            if (r < nr)
+                *reinterpret_cast<uint4*>(y + r * ldy + at) = *reinterpret_cast<const uint4*>(box + r * 128 + ((c ^ (r & 7)) << 4));
+        }
+        return;
+    }
     constexpr int kCols = 128 / (int)sizeof(T);
     for (int c = lane; c < kCols; c += 32) {
         if (col + c >= N) break;
@@ -195,19 +209,19 @@ __device__ __forceinline__ void store_box(const uint8_t* box, T* y, int64_t ldy,
     }
 }
 
-template <bool kPair, class T>
+template <int C, int H, class T>
 __global__ void __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
                const __grid_constant__ CUtensorMap ymap, const bool wide, const Product p)
 {
-    constexpr int C = kPair ? 2 : 1;          // CTAs a tile
-    constexpr int kRows = C * kBlk;           // its rows
-    constexpr int H = C;                      // its columns: H halves of 128
+    using Sm = Smem<C, H>;
+    constexpr bool kPair = C == 2;
+    constexpr int kRows = C * kBlk, S = Sm::kStages;
     constexpr int kBuf = H * kBlk, kBufs = kTmemCols / kBuf;  // a block's product, and how many of them TMEM holds
-    constexpr int S = kStages;
-    constexpr int kCols = kPair ? 128 : 64;   // columns that a promotion thread owns: a half, or half of the only one
+    constexpr int kCols = H * 64;                             // columns that a promotion thread owns
+    constexpr int kIssuers = H > C ? 1 : 2;
     extern __shared__ uint8_t smem_raw[];
-    Smem* sm = reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Sm* sm = reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = kPair ? (int)cluster_rank() : 0;
     const int KB = (p.K + kBlk - 1) / kBlk, nb = (p.N + kBlk - 1) / kBlk, ntiles = (nb + H - 1) / H;
@@ -248,7 +262,7 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
         if (warp == 0) {
             int64_t total;
             if (p.groups) {
-                load_groups<kRows>(p, sm, lane);
+                load_groups<C, H>(p, sm, lane);
                 total = (int64_t)sm->tiles[p.groups] * ntiles;
             } else {
                 total = (p.M + kRows - 1) / kRows * ntiles;
@@ -296,7 +310,7 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                     mbar_arrive(&sm->tfull[b]);
                 }
                 const int w0 = g * p.N + n0 + rank * kBlk;
-                const uint32_t tx = kPair ? (second ? 4 : 3) * kTileBytes : 2 * kTileBytes;
+                const uint32_t tx = kPair ? (second ? 4 : 3) * kTileBytes : kTileBytes + Sm::kWeights;
                 for (int kb = 0; kb < KB; ++kb, ++sc) {
                     const int s = sc % S;
                     if (sc >= S && !warp_wait(&sm->empty[s], (sc / S - 1) & 1, &sm->abort, p.err, 2)) {
@@ -312,7 +326,9 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                         } else {
                             mbar_expect_tx(&sm->full[s], tx);
                             tc5::tma_load_2d(sm->ring[s], &amap, kb * kBlk, (int)row0, &sm->full[s]);
-                            tc5::tma_load_2d(sm->ring[s] + kTileBytes, &wmap, kb * kBlk, w0, &sm->full[s]);
+#pragma unroll
+                            for (int h = 0; h < H; ++h)
+                                tc5::tma_load_2d(sm->ring[s] + (1 + h) * kTileBytes, &wmap, kb * kBlk, w0 + h * kBlk, &sm->full[s]);
                         }
                     }
                     __syncwarp();
@@ -322,11 +338,12 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
             if (rank == 0)
                 for (int i = max(sc - S, 0); i < sc; ++i) wait_drain(&sm->full[i % S], (i / S) & 1);
         } else if (warp <= kIssuers) {
-            // Two warps issue in turn, a block of K each: its MMAs run for 515 clocks, but what one warp does for it
-            // (three waits, eight MMAs, three commits) takes longer.  A warp walks together and one lane issues: in a
+            // Two warps issue in turn, a block of K each: its MMAs run for 515 clocks (a pair) or 288, but what one warp
+            // does for it (two waits, four MMAs, two commits) takes about 600.  (The MMAs of a single CTA's wide tile
+            // wait for shared memory longer than that: one warp.)  A warp walks together and one lane issues: in a
             // branch of one lane the same loop takes half as long again.  Each warp keeps to its own buffers and ring
             // stages, so that no phase of a barrier passes unseen.
-            static_assert(kIssuers == 2 && kStages % 2 == 0 && kBufs % 2 == 0, "ownership");
+            static_assert(S % kIssuers == 0 && kBufs % kIssuers == 0, "ownership");
             const uint64_t ring_desc = tc5::smem_desc_sw128(sm->ring[0]);
             int sc = 0, mine = warp - 1, tc = 0, last = -1;  // blocks of K so far, this warp's next; its last buffer
             bool ok = true;
@@ -345,7 +362,7 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                     ok = warp_wait2(&sm->full[s], (mine / S) & 1, &sm->acce[d], (mine / kBufs) & 1, &sm->abort, p.err, 4);
                     if (!ok) break;
                     tc5::after_sync();
-                    const uint64_t ad = ring_desc + (uint64_t)(s * (2 * kTileBytes >> 4)), wd = ad + (kTileBytes >> 4);
+                    const uint64_t ad = ring_desc + (uint64_t)(s * ((kTileBytes + Sm::kWeights) >> 4)), wd = ad + (kTileBytes >> 4);
                     const uint32_t dt = tmem + d * kBuf;
                     if (elect()) {
 #pragma unroll
@@ -370,9 +387,8 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
-        // a pair's warps 4..7 take the first half of the columns and 8..11 the second; of a single CTA's tile they take
-        // 64 columns each
-        const int quarter = warp & 3, set = (warp - 4) >> 2, half = kPair ? set : 0;
+        // warps 4..7 take the first half of the tile's columns and 8..11 the second
+        const int quarter = warp & 3, set = (warp - 4) >> 2, half = H == 2 ? set : 0;
         const int row = quarter * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + set * kCols;
         const uint32_t acce = peer_addr(&sm->acce[0], 0);  // of the CTA that issues
@@ -453,7 +469,7 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
             constexpr int kBox = 128 / (int)sizeof(T);           // columns of a box
             constexpr int kRound = kOutBytes / (32 * 128);       // boxes staged at once
             const int64_t y0 = ti.row0 + quarter * 32;
-            const int nr = min(ti.nr - quarter * 32, 32), n0 = ti.n0 + half * kBlk + (kPair ? 0 : set * kCols);
+            const int nr = min(ti.nr - quarter * 32, 32), n0 = ti.n0 + set * kCols;
             more = next();
             if (nr <= 0) continue;
             // a box whose rows are all the tile's, or behind the matrix, is left to the copy engine
@@ -470,7 +486,7 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
 #pragma unroll
                 for (int b = b0; b < b0 + kRound && b < kCols / kBox; ++b) {
                     const int col = n0 + b * kBox;
-                    if (!engine) store_box<T>(out + (b - b0) * 32 * 128, static_cast<T*>(p.y) + y0 * p.ldy, p.ldy, nr, col, p.N, lane);
+                    if (!engine) store_box<T>(out + (b - b0) * 32 * 128, static_cast<T*>(p.y) + y0 * p.ldy, p.ldy, nr, col, p.N, wide, lane);
                     else if (lane == 0 && col < p.N) tma_store_2d(&ymap, out + (b - b0) * 32 * 128, col, (int)y0);
                 }
                 if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
@@ -498,7 +514,8 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
 constexpr int kRing = 8;                     // weight tiles in flight: 128 KB of the about 66 KB an SM needs
 constexpr int kOperand = 64 * 1024;          // codes of the activation rows, as many blocks of K as fit
 constexpr int kSBufs = 4;                    // TMEM buffers
-constexpr int kSThreads = 192;               // producer, MMA, four promotion warps
+constexpr int kQuantWarps = 12;              // encode the activation rows; the first four are the promotion warps
+constexpr int kSThreads = 64 + 32 * kQuantWarps;  // with a producer and an MMA warp
 
 template <int NT>
 struct SmallSmem {
@@ -509,6 +526,58 @@ struct SmallSmem {
     uint32_t tmem;
     int abort;
 };
+
+// Codes and scales of the activation rows of n blocks of K, those of this CTA from its i0-th on, into the operand buffer: a
+// half warp per (row, block).
+template <int NT>
+__device__ __forceinline__ void encode_rows(const Product& p, SmallSmem<NT>* sm, int rank, int C, int KB, int i0, int n, int pt) {
+    constexpr int kBatch = 4;                // items in flight a half warp
+    constexpr int kStep = 2 * kQuantWarps;   // half warps
+    const int m = (int)p.M, hl = pt & 15;
+    const float inv = __fdividef(1.0f, (float)m);
+    // (both half warps of a warp make the same turns: they meet in the shuffles)
+    for (int jw = pt >> 5 << 1; jw < n * m; jw += kStep * kBatch) {
+        const int j0 = jw + (pt >> 4 & 1);
+        uint4 raw[kBatch] = {};
+        float sc[kBatch];
+        uint2 code[kBatch];
+        int at[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (jw + kStep * u >= n * m) continue;
+            const int j = min(j0 + kStep * u, n * m - 1);                 // the last one may be read by both
+            const int r = (int)(((float)j + 0.5f) * inv), t = j - r * m;  // exact: j is below 2^12
+            const int kb = rank + (i0 + r) * C, col = kb * kBlk + hl * 8;
+            at[u] = r * NT + t;
+            if (p.x) {
+                if (col < p.K) raw[u] = *reinterpret_cast<const uint4*>(p.x + t * p.ldx + col);
+            } else {
+                if (col < p.K) {
+                    const uint2 q = *reinterpret_cast<const uint2*>(p.a + (int64_t)t * p.K + col);
+                    raw[u].x = q.x;
+                    raw[u].y = q.y;
+                }
+                sc[u] = p.sa[(int64_t)t * KB + kb];
+            }
+        }
+        if (p.x) {
+            encode<kBatch>((n * m - jw + kStep - 1) / kStep, [&](int u) { return amax_bf16(raw[u]); },
+                           [&](int u, float (&v)[8]) { unpack8(raw[u], v); }, sc, code);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) code[u] = make_uint2(raw[u].x, raw[u].y);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (jw + kStep * u >= n * m) continue;
+            if (hl == 0) (&sm->sx[0][0])[at[u]] = sc[u];
+            // 128-byte swizzle: 16-byte chunk c of row t lies at chunk c ^ (t & 7) (NT is a multiple of 8)
+            *reinterpret_cast<uint2*>(sm->b + at[u] * kBlk + (((hl >> 1) ^ (at[u] & 7)) << 4) + (hl & 1) * 8) = code[u];
+        }
+    }
+    fence_async_smem();
+    mbar_arrive(&sm->ready);
+}
 
 // NT: rows rounded up to 16, 32 or 64.  The cluster's CTA r takes the blocks kb = r, r + C, ...
 template <int NT, class T>
@@ -533,7 +602,7 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
             mbar_init(&sm->accf[i], 1);
             mbar_init(&sm->acce[i], 4);
         }
-        mbar_init(&sm->ready, 128);
+        mbar_init(&sm->ready, 32 * kQuantWarps);
         mbar_init(&sm->drained, 4);
         sm->abort = 0;
         async::fence_barrier_init();
@@ -581,6 +650,11 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
             __syncwarp();
         }
         if (i > 0) wait_drain(&sm->accf[(i - 1) % kSBufs], ((i - 1) / kSBufs) & 1);
+    } else if (warp >= 6) {
+        for (int i0 = 0; i0 < mine; i0 += kRound) {
+            if (i0 > 0 && !warp_wait(&sm->drained, (i0 / kRound - 1) & 1, &sm->abort, p.err, 18)) break;
+            encode_rows<NT>(p, sm, rank, C, KB, i0, min(kRound, mine - i0), tid - 64);
+        }
     } else {
         const int pt = tid - 64, quarter = warp & 3;
         const int row = quarter * 32 + lane;  // weight row of the tile
@@ -596,52 +670,8 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
                 if (lane == 0) mbar_arrive(&sm->drained);
                 if (!warp_wait(&sm->drained, (i0 / kRound - 1) & 1, &sm->abort, p.err, 17)) break;
             }
-            // operand rows of this round: a half warp per (row, block)
             const int n = min(kRound, mine - i0);
-            const int hl = pt & 15;
-            constexpr int kBatch = NT == 16 ? 4 : 8;  // (row, block) items in flight a half warp
-            const float inv = __fdividef(1.0f, (float)m);
-            // (both half warps of a warp make the same turns: they meet in the shuffles)
-            for (int jw = pt >> 5 << 1; jw < n * m; jw += 8 * kBatch) {
-                const int j0 = jw + (pt >> 4 & 1);
-                uint4 raw[kBatch] = {};
-                float sc[kBatch];
-                int at[kBatch];
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    if (jw + 8 * u >= n * m) continue;
-                    const int j = min(j0 + 8 * u, n * m - 1);            // the last one may be read by both
-                    const int r = (int)(((float)j + 0.5f) * inv), t = j - r * m;  // exact: j is below 2^12
-                    const int kb = rank + (i0 + r) * C, col = kb * kBlk + hl * 8;
-                    at[u] = r * NT + t;
-                    if (p.x) {
-                        if (col < p.K) raw[u] = *reinterpret_cast<const uint4*>(p.x + t * p.ldx + col);
-                    } else {
-                        if (col < p.K) {
-                            const uint2 q = *reinterpret_cast<const uint2*>(p.a + (int64_t)t * p.K + col);
-                            raw[u].x = q.x;
-                            raw[u].y = q.y;
-                        }
-                        sc[u] = p.sa[(int64_t)t * KB + kb];
-                    }
-                }
-                uint2 code[kBatch];
-                if (p.x) {
-                    encode<kBatch>((n * m - jw + 7) / 8, [&](int u, float (&v)[8]) { unpack8(raw[u], v); }, sc, code);
-                } else {
-#pragma unroll
-                    for (int u = 0; u < kBatch; ++u) code[u] = make_uint2(raw[u].x, raw[u].y);
-                }
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    if (jw + 8 * u >= n * m) continue;
-                    if (hl == 0) (&sm->sx[0][0])[at[u]] = sc[u];
-                    // 128-byte swizzle: 16-byte chunk c of row t lies at chunk c ^ (t & 7) (NT is a multiple of 8)
-                    *reinterpret_cast<uint2*>(sm->b + at[u] * kBlk + (((hl >> 1) ^ (at[u] & 7)) << 4) + (hl & 1) * 8) = code[u];
-                }
-            }
-            fence_async_smem();
-            mbar_arrive(&sm->ready);
+            encode_rows<NT>(p, sm, rank, C, KB, i0, n, pt);
             if (!warp_wait(&sm->ready, (i0 / kRound) & 1, &sm->abort, p.err, 15)) break;
             float ws = sw[(int64_t)i0 * C];
             bool ok = true;
@@ -700,11 +730,11 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
         if (warp >= 2 && !sm->abort) {
             // every C-th row is this CTA's: a warp a row, two rows and all the peers' sums in flight
             const int c4 = lane * 4, col = nt * kBlk + c4;
-            for (int i0 = warp - 2; rank + C * i0 < m; i0 += 8) {
+            for (int i0 = warp - 2; rank + C * i0 < m; i0 += 2 * kQuantWarps) {
                 float4 v[2][8];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int t = rank + C * (i0 + 4 * u);
+                    const int t = rank + C * (i0 + kQuantWarps * u);
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
                         if (c < C && t < m)
@@ -712,7 +742,7 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int t = rank + C * (i0 + 4 * u);
+                    const int t = rank + C * (i0 + kQuantWarps * u);
                     if (t >= m) continue;
                     float4 sum = v[u][0];
 #pragma unroll
@@ -763,7 +793,7 @@ cudaError_t launch(unsigned grid, unsigned threads, size_t smem, int cluster, cu
     return cudaLaunchKernelEx(&cfg, kKernel, args...);
 }
 
-template <bool kPair>
+template <int C, int H>
 cudaError_t launch_many(const Product& p, const CUtensorMap& am, const CUtensorMap& wm, int64_t tiles, cudaStream_t st) {
     // y for the copy engine, where it is laid out for it: it writes whole 16 bytes, past the last column too
     const int64_t es = p.y_bf16 ? 2 : 4;
@@ -773,11 +803,10 @@ cudaError_t launch_many(const Product& p, const CUtensorMap& am, const CUtensorM
         const cudaError_t e = out_map(&ym, p.y, (uint64_t)p.N, (uint64_t)p.M, (uint64_t)(p.ldy * es), p.y_bf16);
         if (e != cudaSuccess) return e;
     }
-    constexpr int C = kPair ? 2 : 1;
     const unsigned grid = (unsigned)std::min<int64_t>(tiles, sm_count() / C) * C;
-    const size_t smem = sizeof(Smem) + 1024;
-    return p.y_bf16 ? launch<product_kernel<kPair, __nv_bfloat16>>(grid, kThreads, smem, C, st, am, wm, ym, wide, p)
-                    : launch<product_kernel<kPair, float>>(grid, kThreads, smem, C, st, am, wm, ym, wide, p);
+    const size_t smem = sizeof(Smem<C, H>) + 1024;
+    return p.y_bf16 ? launch<product_kernel<C, H, __nv_bfloat16>>(grid, kThreads, smem, C, st, am, wm, ym, wide, p)
+                    : launch<product_kernel<C, H, float>>(grid, kThreads, smem, C, st, am, wm, ym, wide, p);
 }
 
 template <int NT>
@@ -799,13 +828,16 @@ cudaError_t launch_product(const Product& p, cudaStream_t st) {
     const auto row_tiles = [&](int64_t rows) {
         return p.groups ? std::min<int64_t>(p.M / rows + p.groups, p.M) : (p.M + rows - 1) / rows;
     };
-    const int64_t nb = blocks_of(p.N), pairs = row_tiles(2 * kBlk) * ((nb + 1) / 2);
-    // pairs of CTAs where there are tiles for all of them
-    const bool pair = nb > 1 && 2 * pairs >= sm_count();
+    const int64_t nb = blocks_of(p.N), wide = (nb + 1) / 2, pairs = row_tiles(2 * kBlk) * wide, singles = row_tiles(kBlk) * wide;
     e = byte_map(&wm, p.w, (uint64_t)p.K, (uint64_t)(G * p.N), (uint64_t)p.K, kBlk);
     if (e != cudaSuccess) return e;
-    if (pair) return launch_many<true>(p, am, wm, pairs, st);
-    return launch_many<false>(p, am, wm, row_tiles(kBlk) * nb, st);
+    // Dense rows go to pairs of CTAs where there are tiles for all of them (32768 x 2048 x 2048: 221 us, 232 us with tiles
+    // of 128 x 256).  Groups fill 256 rows less often (8192 rows in 60 groups: 24 us with tiles of 128 x 256, 30 us with
+    // pairs; 32768 rows: 127 us and 130 us).  Where there are too few of either, tiles of 128 x 128 (777 x 1000 x 784: 9.5
+    // us, 12 us with the others).
+    if (nb > 1 && !p.groups && 2 * pairs >= sm_count()) return launch_many<2, 2>(p, am, wm, pairs, st);
+    if (nb > 1 && singles >= sm_count()) return launch_many<1, 2>(p, am, wm, singles, st);
+    return launch_many<1, 1>(p, am, wm, row_tiles(kBlk) * nb, st);
 }
 
 cudaError_t launch_product_small(const Product& p, cudaStream_t st) {

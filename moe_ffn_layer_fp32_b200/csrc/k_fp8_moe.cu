@@ -581,10 +581,16 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
                 }
                 float scale[4];
                 uint2 code[4];
-                encode<4>((own - jw + 7) / 8, [&](int u, float (&v)[8]) {
+                const auto get = [&](int u, float (&v)[8]) {
                     v[0] = a[u].x; v[1] = a[u].y; v[2] = a[u].z; v[3] = a[u].w;
                     v[4] = b[u].x; v[5] = b[u].y; v[6] = b[u].z; v[7] = b[u].w;
-                }, scale, code);
+                };
+                const auto peak = [&](int u) {
+                    float v[8];
+                    get(u, v);
+                    return amax8(v);
+                };
+                encode<4>((own - jw + 7) / 8, peak, get, scale, code);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     if (jw + 8 * u >= own) continue;

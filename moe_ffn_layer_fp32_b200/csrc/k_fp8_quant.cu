@@ -12,6 +12,27 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kItems = 4;  // blocks a half warp holds at once: enough loads in flight to cover the latency
 
+// 8 values as they lie in memory (zeros until loaded).
+template <class T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+    float v[8] = {};
+    __device__ __forceinline__ void load(const float* p) { load8(p, v); }
+    __device__ __forceinline__ uint32_t amax() const { return amax8(v); }
+    __device__ __forceinline__ void get(float (&o)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = v[j];
+    }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 u = {0u, 0u, 0u, 0u};
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ uint32_t amax() const { return amax_bf16(u); }
+    __device__ __forceinline__ void get(float (&o)[8]) const { unpack8(u, o); }
+};
+
 // Rows: a half warp takes one (row, block) at a time, 8 values a lane (16 bytes of BF16).
 template <class T>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const T* x, int64_t nblk, int kb, int K,
@@ -25,30 +46,28 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const T* x, int
     const int64_t begin = (int64_t)blockIdx.x * kPer, row0 = begin / kb;
     const int b0 = (int)(begin - row0 * kb), mine = (threadIdx.x >> 4) * kItems;
     const int64_t first = begin + mine;
-    float v[kItems][8];
-    int64_t row[kItems];
-    int col[kItems];
+    Raw8<T> v[kItems];
+    int64_t at[kItems];  // of the lane's values in q (-1: none)
+    int64_t row = row0 + (b0 + mine) / kb;  // 64-bit divisions for each block took three times the copy's time
+    int col = (b0 + mine) % kb * kBlk + hl * 8;
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-        const int64_t b = first + i;
-        const int at = b0 + mine + i, down = at / kb;  // 64-bit divisions for each block took three times the copy's time
-        row[i] = row0 + down;
-        col[i] = (at - down * kb) * kBlk + hl * 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-        if (b < nblk && col[i] < K) load8(x + row[i] * ldx + col[i], v[i]);
+        const bool in = first + i < nblk && col < K;
+        at[i] = in ? row * K + col : -1;
+        if (in) v[i].load(x + row * ldx + col);
+        col += kBlk;
+        if (col >= kb * kBlk) {
+            col = hl * 8;
+            ++row;
+        }
     }
     float sc[kItems];
     uint2 code[kItems];
-    encode<kItems>(kItems, [&](int i, float (&o)[8]) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = v[i][j];
-    }, sc, code);
+    encode<kItems>(kItems, [&](int i) { return v[i].amax(); }, [&](int i, float (&o)[8]) { v[i].get(o); }, sc, code);
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-        if (first + i >= nblk) continue;
-        if (hl == 0) s[first + i] = sc[i];
-        if (col[i] < K) *reinterpret_cast<uint2*>(q + row[i] * K + col[i]) = code[i];
+        if (hl == 0 && first + i < nblk) s[first + i] = sc[i];
+        if (at[i] >= 0) *reinterpret_cast<uint2*>(q + at[i]) = code[i];
     }
 }
 
