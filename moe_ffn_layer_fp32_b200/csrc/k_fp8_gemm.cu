@@ -511,11 +511,21 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
 
 // -------------------------------------------------------------------- few rows
 
-constexpr int kRing = 8;                     // weight tiles in flight: 128 KB of the about 66 KB an SM needs
-constexpr int kOperand = 64 * 1024;          // codes of the activation rows, as many blocks of K as fit
+// A ring of 64 KB (an SM needs about 66 KB in flight) and the codes of 32 KB of activation rows, as many blocks of K as
+// fit: less than half an SM's shared memory, so that the next launch of a chain gets ready beside this one.
+constexpr int kRing = 4;
+constexpr int kOperand = 32 * 1024;
 constexpr int kSBufs = 4;                    // TMEM buffers
-constexpr int kQuantWarps = 12;              // encode the activation rows; the first four are the promotion warps
-constexpr int kSThreads = 64 + 32 * kQuantWarps;  // with a producer and an MMA warp
+
+// Warps that encode the activation rows; the first four go on as the promotion warps.
+template <int NT>
+constexpr int quant_warps() {
+    return NT == 16 ? 4 : NT == 32 ? 8 : 12;
+}
+template <int NT>
+constexpr int small_threads() {
+    return 64 + 32 * quant_warps<NT>();      // with a producer and an MMA warp
+}
 
 template <int NT>
 struct SmallSmem {
@@ -532,7 +542,7 @@ struct SmallSmem {
 template <int NT>
 __device__ __forceinline__ void encode_rows(const Product& p, SmallSmem<NT>* sm, int rank, int C, int KB, int i0, int n, int pt) {
     constexpr int kBatch = 4;                // items in flight a half warp
-    constexpr int kStep = 2 * kQuantWarps;   // half warps
+    constexpr int kStep = 2 * quant_warps<NT>();  // half warps
     const int m = (int)p.M, hl = pt & 15;
     const float inv = __fdividef(1.0f, (float)m);
     // (both half warps of a warp make the same turns: they meet in the shuffles)
@@ -581,7 +591,7 @@ __device__ __forceinline__ void encode_rows(const Product& p, SmallSmem<NT>* sm,
 
 // NT: rows rounded up to 16, 32 or 64.  The cluster's CTA r takes the blocks kb = r, r + C, ...
 template <int NT, class T>
-__global__ void __launch_bounds__(kSThreads, 1)
+__global__ void __launch_bounds__(small_threads<NT>(), 1)
 product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, const int C)
 {
     constexpr int kRound = kOperand / (NT * kBlk);  // blocks of K the operand buffer holds
@@ -602,7 +612,7 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
             mbar_init(&sm->accf[i], 1);
             mbar_init(&sm->acce[i], 4);
         }
-        mbar_init(&sm->ready, 32 * kQuantWarps);
+        mbar_init(&sm->ready, 32 * quant_warps<NT>());
         mbar_init(&sm->drained, 4);
         sm->abort = 0;
         async::fence_barrier_init();
@@ -730,11 +740,11 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
         if (warp >= 2 && !sm->abort) {
             // every C-th row is this CTA's: a warp a row, two rows and all the peers' sums in flight
             const int c4 = lane * 4, col = nt * kBlk + c4;
-            for (int i0 = warp - 2; rank + C * i0 < m; i0 += 2 * kQuantWarps) {
+            for (int i0 = warp - 2; rank + C * i0 < m; i0 += 2 * quant_warps<NT>()) {
                 float4 v[2][8];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int t = rank + C * (i0 + kQuantWarps * u);
+                    const int t = rank + C * (i0 + quant_warps<NT>() * u);
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
                         if (c < C && t < m)
@@ -742,7 +752,7 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int t = rank + C * (i0 + kQuantWarps * u);
+                    const int t = rank + C * (i0 + quant_warps<NT>() * u);
                     if (t >= m) continue;
                     float4 sum = v[u][0];
 #pragma unroll
@@ -813,8 +823,8 @@ template <int NT>
 cudaError_t launch_few(const Product& p, const CUtensorMap& wm, int C, cudaStream_t st) {
     const unsigned grid = (unsigned)(blocks_of(p.N) * C);
     const size_t smem = sizeof(SmallSmem<NT>) + 1024;
-    return p.y_bf16 ? launch<product_small_kernel<NT, __nv_bfloat16>>(grid, kSThreads, smem, C, st, wm, p, C)
-                    : launch<product_small_kernel<NT, float>>(grid, kSThreads, smem, C, st, wm, p, C);
+    return p.y_bf16 ? launch<product_small_kernel<NT, __nv_bfloat16>>(grid, small_threads<NT>(), smem, C, st, wm, p, C)
+                    : launch<product_small_kernel<NT, float>>(grid, small_threads<NT>(), smem, C, st, wm, p, C);
 }
 
 }  // namespace
