@@ -591,7 +591,7 @@ __device__ __forceinline__ void encode_rows(const Product& p, SmallSmem<NT>* sm,
 
 // NT: rows rounded up to 16, 32 or 64.  The cluster's CTA r takes the blocks kb = r, r + C, ...
 template <int NT, class T>
-__global__ void __launch_bounds__(small_threads<NT>(), 1)
+__global__ void __launch_bounds__(small_threads<NT>(), NT == 64 ? 1 : 2)
 product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, const int C)
 {
     constexpr int kRound = kOperand / (NT * kBlk);  // blocks of K the operand buffer holds

@@ -53,22 +53,32 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
 }
 
 // 1 / sqrt(mean(v^2) + eps) of the row that kG threads hold.  `part` holds one word a warp; the next row uses another
-// one, so that one barrier is enough.
+// one, so that one barrier is enough.  Every thread does the last steps, so they are a product with 1 / d (inv_d) and
+// rsqrtf (off by 2 ulp at most): with IEEE divisions and root the kernel issued 430 instructions a warp and row, and
+// was bound by them.
 template <int kG>
-__device__ __forceinline__ float inv_rms(const float (&v)[8], float* part, int d, float eps) {
+__device__ __forceinline__ float inv_rms(const float (&v)[8], float* part, float inv_d, float eps) {
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (kG > 32) {
+        constexpr int kW = kG / 32;
         if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
         __syncthreads();
-        sum = 0.0f;
+        if constexpr (kW % 4 == 0) {
+            sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kG / 32; ++i) sum += part[i];
+            for (int i = 0; i < kW; i += 4) {
+                const float4 p = *reinterpret_cast<const float4*>(part + i);
+                sum += (p.x + p.y) + (p.z + p.w);
+            }
+        } else {
+            sum = part[0] + part[1];
+        }
     }
-    return __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(sum, (float)d) + eps));
+    return rsqrtf(fmaf(sum, inv_d, eps));
 }
 
 // kG threads a row; a CTA has one row, or eight of a warp each.
@@ -87,7 +97,7 @@ template <int kG, class R, class Y>
 __global__ void __launch_bounds__(threads<kG>(), resident<kG>()) block_norm_kernel(const NormPlan p)
 {
     constexpr int kRows = threads<kG>() / kG;
-    __shared__ float part[2][2][kG / 32];
+    __shared__ alignas(16) float part[2][2][kG / 32];
     const int g = threadIdx.x % kG, c = g * 8;
     const bool mine = c < p.d;
     f8::dep_launch();
@@ -114,6 +124,7 @@ __global__ void __launch_bounds__(threads<kG>(), resident<kG>()) block_norm_kern
         if (p.w_pre) pre.load(p.w_pre + c);
     }
     const int kb = (p.d + f8::kBlk - 1) / f8::kBlk;
+    const float inv_d = __fdiv_rn(1.0f, (float)p.d);
     for (int turn = 0; row < p.rows; row += step, turn ^= 1) {  // the same row for all kG threads
         float r[8], z[8], w[8];
         rr.get(r);
@@ -123,7 +134,7 @@ __global__ void __launch_bounds__(threads<kG>(), resident<kG>()) block_norm_kern
         gate.get(gv);
         if (row + step < p.rows) fetch(row + step);
         if (p.w_post) {
-            const float s = inv_rms<kG>(z, part[turn][0], p.d, p.eps);
+            const float s = inv_rms<kG>(z, part[turn][0], inv_d, p.eps);
             post.get(w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) z[j] = z[j] * s * w[j];
@@ -139,7 +150,7 @@ __global__ void __launch_bounds__(threads<kG>(), resident<kG>()) block_norm_kern
         for (int j = 0; j < 8; ++j) r[j] = block ? fmaf(p.scale, r[j], z[j]) : p.scale * r[j];
         if (p.r_out && mine) store8(static_cast<R*>(p.r_out) + row * p.ldo + c, r);
         if (!p.w_pre) continue;
-        const float s = inv_rms<kG>(r, part[turn][1], p.d, p.eps);
+        const float s = inv_rms<kG>(r, part[turn][1], inv_d, p.eps);
         pre.get(w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[j] = r[j] * s * w[j];
