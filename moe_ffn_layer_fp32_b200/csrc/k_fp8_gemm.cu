@@ -541,7 +541,7 @@ struct SmallSmem {
 // half warp per (row, block).
 template <int NT>
 __device__ __forceinline__ void encode_rows(const Product& p, SmallSmem<NT>* sm, int rank, int C, int KB, int i0, int n, int pt) {
-    constexpr int kBatch = 4;                // items in flight a half warp
+    constexpr int kBatch = NT == 16 ? 2 : 4;      // items in flight a half warp
     constexpr int kStep = 2 * quant_warps<NT>();  // half warps
     const int m = (int)p.M, hl = pt & 15;
     const float inv = __fdividef(1.0f, (float)m);

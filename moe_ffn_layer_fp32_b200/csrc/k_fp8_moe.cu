@@ -11,8 +11,8 @@
 // the eight partial logits through distributed shared memory in a fixed order,
 // gating, top-k; it also quantises that token's x.
 //
-// moe_experts_kernel: a cluster of S CTAs takes one expert and up to 16 of its
-// tokens (the tensor cores' smallest N).  A shared expert wider than the routed
+// moe_experts_kernel: a cluster of S CTAs takes one expert and up to 8 of its
+// tokens (half of the tensor cores' smallest N: wider clusters are the last to end).  A shared expert wider than the routed
 // ones is taken in parts of its hidden features, a cluster each, so that it is
 // not what the others wait for.  Weights are the MMA's M: a tile is up to 128
 // weight rows x 128 of K, one copy, one step of a ring that runs from the first
@@ -49,7 +49,7 @@ using async::mbar_init;
 constexpr int kRouteCluster = 8;
 constexpr int kRouteThreads = 512;
 constexpr int kRouteParts = kRouteThreads / 64;  // K parts within a CTA
-constexpr int kRouteAhead = 16;                  // router weights a thread has in flight
+constexpr int kRouteAhead = 32;                  // router weights a thread has in flight
 
 // ------------------------------------------------------------------ router
 
@@ -166,28 +166,31 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
 
 // ----------------------------------------------------------------- experts
 
-constexpr int kN = 16;                 // tokens of a cluster
+constexpr int kN = 8;                  // tokens of a cluster
+constexpr int kCols = 16;              // the tokens' side of an MMA, its smallest: the other half is not used
 constexpr int kThreads = 224;          // producer, MMA, four promotion warps, MMA
 constexpr int kSlot = kBlk * kBlk;     // a ring slot: 16 KB
-constexpr int kMinRing = 2, kMaxRing = 12;  // even: each of the two MMA warps keeps to its own slots and buffers
+constexpr int kMinRing = 2, kMaxRing = 12;
 constexpr int kBufs = 8;               // TMEM buffers of 16 columns
-constexpr int kTmemCols = kBufs * kN;
+constexpr int kTmemCols = kBufs * kCols;
 constexpr int kUnit = 16;              // hidden features of a lane quarter
 constexpr int kAlone = 16;             // (token, block) items that each CTA quantises for itself
 
-// Dynamic shared memory: ring | operand codes (x, then the hidden features) | own hidden features
-// [16][features of a rank] | scales of x | scales of the hidden features.
+// Dynamic shared memory: ring | operand codes (x, then the hidden features: 8 rows a block of 128; the MMA's other 8 rows
+// are the next block's, or the 1 KB behind the last) | own hidden features [8][features of a rank] | scales of x | scales
+// of the hidden features.
 struct Layout {
-    int ring;        // slots
-    int nu[2], no;   // units of 16 features (routed, shared) and of 32 output rows in a tile
-    int operand;     // byte offsets
+    int ring;              // slots
+    int issuers;           // MMA warps: two, each with its own slots and buffers, or one for an odd ring
+    int nu[2], no;         // units of 16 features (routed, shared) and of 32 output rows in a tile
+    int operand;           // byte offsets
     int hidden, hidden_ld;
     int sx, sh;
     int bytes;
 };
 
 struct ExpertShared {
-    uint64_t full[kMaxRing], empty[kMaxRing], accf[kBufs], acce[kBufs], xready, hready, pbar, peers, codes;
+    uint64_t full[kMaxRing], empty[kMaxRing], accf[kBufs], acce[kBufs], xready, hready, stored, counted, peers, codes;  // from xready on: one phase each
     uint32_t tmem;
     int abort;
     int count[kMaxExperts];
@@ -205,12 +208,12 @@ __device__ __forceinline__ void peer_store(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// 16-byte chunk c of operand row t lies at chunk c ^ (t & 7) (128-byte swizzle).
-__device__ __forceinline__ uint8_t* operand_at(uint8_t* base, int kb, int t, int byte) {
-    return base + (kb * kN + t) * kBlk + (((byte >> 4) ^ (t & 7)) << 4) + (byte & 15);
+// 16-byte chunk c of operand row t lies at chunk c ^ (t & 7) (128-byte swizzle); `row` counts over all blocks.
+__device__ __forceinline__ uint8_t* operand_at(uint8_t* base, int row, int byte) {
+    return base + row * kBlk + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 15);
 }
 
-// Thread pt (of 128) of one TMEM tile: adds the 16 columns of its row, scaled.
+// Thread pt (of 128) of one TMEM tile: adds the 8 columns of its row, scaled.
 __device__ __forceinline__ void add_scaled(float2 (&acc)[kN / 2], const uint32_t (&v)[kN], const float* s, float w) {
 #pragma unroll
     for (int c = 0; c < kN / 2; ++c) {
@@ -218,6 +221,18 @@ __device__ __forceinline__ void add_scaled(float2 (&acc)[kN / 2], const uint32_t
         acc[c] = __ffma2_rn(make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])),
                             make_float2(s2.x * w, s2.y * w), acc[c]);
     }
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld8(uint32_t (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
 }
 
 __device__ __forceinline__ float2 first_two(const float* w, int KB) { return make_float2(w[0], w[KB > 1 ? 1 : 0]); }
@@ -232,13 +247,13 @@ __device__ __forceinline__ bool add_blocks(float2 (&acc)[kN / 2], ExpertShared* 
     uint32_t v[2][kN];
     if (!warp_wait(&sm->accf[i % kBufs], (i / kBufs) & 1, &sm->abort, err, site)) return false;
     tc5::after_sync();
-    tc5::tmem_ld16(tl + i % kBufs * kN, v[0]);
+    tmem_ld8(tl + i % kBufs * kCols, v[0]);
     for (int kb0 = 0; kb0 < KB; kb0 += 2) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int kb = kb0 + u;
             if (kb >= KB) break;
-            tc5::tmem_wait_ld(v[u]);
+            tmem_wait_ld8(v[u]);
             tc5::before_sync();
             __syncwarp();
             if ((threadIdx.x & 31) == 0) mbar_arrive(&sm->acce[(i + kb) % kBufs]);
@@ -249,7 +264,7 @@ __device__ __forceinline__ bool add_blocks(float2 (&acc)[kN / 2], ExpertShared* 
                 const int n = i + kb + 1;
                 if (!warp_wait(&sm->accf[n % kBufs], (n / kBufs) & 1, &sm->abort, err, site)) return false;
                 tc5::after_sync();
-                tc5::tmem_ld16(tl + n % kBufs * kN, v[u ^ 1]);
+                tmem_ld8(tl + n % kBufs * kCols, v[u ^ 1]);
             }
             add_scaled(acc, v[u], s + kb * kN, wc);
         }
@@ -388,7 +403,8 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
         }
         mbar_init(&sm->xready, 128);
         mbar_init(&sm->hready, 128);
-        mbar_init(&sm->pbar, 4);
+        mbar_init(&sm->stored, 4);
+        mbar_init(&sm->counted, 4);
         mbar_init(&sm->peers, S * 4);
         mbar_init(&sm->codes, S * 4);
         sm->abort = 0;
@@ -460,7 +476,7 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
         for (int j = max(i - lay.ring, 0); j < i; ++j) wait_drain(&sm->full[j % lay.ring], (j / lay.ring) & 1);
     } else if (warp == 1 || warp == 6) {
         int last = -1;
-        for (int i = warp == 1 ? 0 : 1; i < steps; i += 2) {
+        for (int i = warp == 1 ? 0 : lay.issuers == 2 ? 1 : steps; i < steps; i += lay.issuers) {
             const int s = i % lay.ring, b = i % kBufs;
             if ((i < 2 && gt > 0 && !warp_wait(&sm->xready, 0, &sm->abort, p.err, 22)) ||
                 ((i == ngu || i == ngu + 1) && !warp_wait(&sm->hready, 0, &sm->abort, p.err, 23)) ||
@@ -473,7 +489,7 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
             if (elect()) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mma_e4m3(tmem + b * kN, wd + 2 * k, bd + 2 * k, idesc_e4m3(kN), k > 0);
+                    mma_e4m3(tmem + b * kCols, wd + 2 * k, bd + 2 * k, idesc_e4m3(kCols), k > 0);
                 tc5::commit(&sm->empty[s]);
                 tc5::commit(&sm->accf[b]);
             }
@@ -500,25 +516,25 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
         };
         float2 gate_up_w = first_two(gate_up_scales(0), KBd), down_w = first_two(down_scales(0), KBh);
         // the tokens' codes and scales; features past d are zeros
-        if ((pt >> 3) < n) {
-            const int t = pt >> 3, c = pt & 7;  // a 16-byte chunk of a token's blocks, eight blocks in flight
+        if ((pt >> 3 & 7) < n) {
+            const int t = pt >> 3 & 7, c = pt & 7;  // a 16-byte chunk of every second block of a token, eight in flight
             const uint8_t* from = p.xq + (int64_t)sm->token[t] * d + c * 16;
-            for (int kb0 = 0; kb0 < KBd; kb0 += 8) {
+            for (int kb0 = pt >> 6; kb0 < KBd; kb0 += 16) {
                 uint4 v[8];
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     v[u] = make_uint4(0u, 0u, 0u, 0u);
-                    if ((kb0 + u) * kBlk + c * 16 < d) v[u] = *reinterpret_cast<const uint4*>(from + (kb0 + u) * kBlk);
+                    if ((kb0 + 2 * u) * kBlk + c * 16 < d) v[u] = *reinterpret_cast<const uint4*>(from + (kb0 + 2 * u) * kBlk);
                 }
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
-                    if (kb0 + u < KBd) *reinterpret_cast<uint4*>(operand_at(operand, kb0 + u, t, c * 16)) = v[u];
+                    if (kb0 + 2 * u < KBd) *reinterpret_cast<uint4*>(operand_at(operand, (kb0 + 2 * u) * kN + t, c * 16)) = v[u];
             }
         }
-        if ((pt & 15) < n) {
-            const float* from = p.sx + sm->token[pt & 15] * KBd;
+        if ((pt & 7) < n) {
+            const float* from = p.sx + sm->token[pt & 7] * KBd;
 #pragma unroll 4
-            for (int kb = pt >> 4; kb < KBd; kb += 8) sx[kb * kN + (pt & 15)] = from[kb];
+            for (int kb = pt >> 3; kb < KBd; kb += 16) sx[kb * kN + (pt & 7)] = from[kb];
         }
         fence_async_smem();
         mbar_arrive(&sm->xready);
@@ -553,56 +569,36 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
             wait_cluster(&sm->peers, 0, &sm->abort, p.err, 32);  // each lane's own acquire
         }
         if (ok) {
-            // A half warp per (token, block), four of them in flight.  With few of them each CTA quantises all for
-            // itself; with more, 1 / S of them for all, at the price of another signal (about 1 us): 128 items took
-            // 8.6 us alone and take 4.0 us shared.
+            // A half warp per (token, block).  With few of them each CTA quantises all for itself; with more, 1 / S of
+            // them for all, at the price of another signal (about 1 us): 128 items took 8.6 us alone and take 4.0 us
+            // shared.  (Four at a time hide more of the peers' latency, but four times the code comes from L2: 2.9 us
+            // for a single item instead of 1.3 us.)
             const int U = H / kUnit, items = n * KBh, stride = items > kAlone ? S : 1, first = items > kAlone ? rank : 0;
             const int own = (items - first + stride - 1) / stride;
-            const float inv = __fdividef(1.0f, (float)KBh);
             // (both half warps of a warp make the same turns: they meet in the shuffles)
-            for (int jw = pt >> 5 << 1; jw < own; jw += 32) {
-                float4 a[4], b[4];
-                int at[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    a[u] = b[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (jw + 8 * u >= own) continue;
-                    const int j = first + stride * min(jw + (pt >> 4 & 1) + 8 * u, own - 1);  // the last one may be read by both
-                    const int t = (int)(((float)j + 0.5f) * inv), kb = j - t * KBh;         // exact: j is at most 16 * 32
-                    const int f = kb * kBlk + hl * 8;
-                    at[u] = kb * kN + t;
-                    if (f < H) {
-                        // the rank that owns unit f / 16: the last one that starts at or before it
-                        const int r = (S * (f / kUnit + 1) - 1) / U;
-                        const uint32_t from = peer_addr(hidden + t * lay.hidden_ld + (f - U * r / S * kUnit), (uint32_t)r);
-                        a[u] = peer_load4(from);
-                        b[u] = peer_load4(from + 16);
-                    }
+#pragma unroll 1
+            for (int jw = pt >> 5 << 1; jw < own; jw += 8) {
+                const int j = first + stride * min(jw + (pt >> 4 & 1), own - 1);  // the last one may be done by both
+                const int t = j / KBh, kb = j - t * KBh, f = kb * kBlk + hl * 8;
+                float v[8] = {};
+                if (f < H) {
+                    // the rank that owns unit f / 16: the last one that starts at or before it
+                    const int r = (S * (f / kUnit + 1) - 1) / U;
+                    const uint32_t from = peer_addr(hidden + t * lay.hidden_ld + (f - U * r / S * kUnit), (uint32_t)r);
+                    const float4 a = peer_load4(from), b = peer_load4(from + 16);
+                    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+                    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
                 }
-                float scale[4];
-                uint2 code[4];
-                const auto get = [&](int u, float (&v)[8]) {
-                    v[0] = a[u].x; v[1] = a[u].y; v[2] = a[u].z; v[3] = a[u].w;
-                    v[4] = b[u].x; v[5] = b[u].y; v[6] = b[u].z; v[7] = b[u].w;
-                };
-                const auto peak = [&](int u) {
-                    float v[8];
-                    get(u, v);
-                    return amax8(v);
-                };
-                encode<4>((own - jw + 7) / 8, peak, get, scale, code);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if (jw + 8 * u >= own) continue;
-                    uint8_t* to = operand + at[u] * kBlk + (((hl >> 1) ^ (at[u] & 7)) << 4) + (hl & 1) * 8;
-                    if (stride == 1) {
-                        *reinterpret_cast<uint2*>(to) = code[u];
-                        if (hl == 0) sh[at[u]] = scale[u];
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < S; ++r) peer_store8(peer_addr(to, (uint32_t)r), code[u]);
-                        if (hl < S) peer_store(peer_addr(sh + at[u], (uint32_t)hl), scale[u]);
-                    }
+                const float s = scale_of(half_warp_max(amax8(v)));
+                const uint2 code = Coder(s)(v);
+                uint8_t* to = operand_at(operand, kb * kN + t, hl * 8);
+                float* st = sh + kb * kN + t;
+                if (stride == 1) {
+                    *reinterpret_cast<uint2*>(to) = code;
+                    if (hl == 0) *st = s;
+                } else {
+                    for (int r = 0; r < S; ++r) peer_store8(peer_addr(to, (uint32_t)r), code);
+                    if (hl < S) peer_store(peer_addr(st, (uint32_t)hl), s);
                 }
             }
             if (stride != 1) {
@@ -635,31 +631,59 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
         // a token's last contribution to this rank's output rows adds them all up
         __threadfence();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->pbar);
-        ok = warp_wait(&sm->pbar, 0, &sm->abort, p.err, 30) && ok;
+        if (lane == 0) mbar_arrive(&sm->stored);
+        ok = warp_wait(&sm->stored, 0, &sm->abort, p.err, 30) && ok;
         if (ok && o1 > o0) {
             if (pt < n) sm->last[pt] = atomicAdd(&p.arrived[sm->token[pt] * kRanks + rank], 1u) == (uint32_t)(p.k + p.parts - 1);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm->pbar);
-            ok = warp_wait(&sm->pbar, 1, &sm->abort, p.err, 31);
+            if (lane == 0) mbar_arrive(&sm->counted);
+        }
+    }
+    // every warp helps with these sums
+    if (o1 > o0) {
+        __syncwarp();
+        if (warp_wait(&sm->counted, 0, &sm->abort, p.err, 31)) {
             __threadfence();
-            for (int j = 0; j < n && ok; ++j) {
+            const int quads = (o1 - o0) * 8;  // four columns a thread
+            const bool wide = (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
+#pragma unroll 1
+            for (int at = tid; at < n * quads; at += kThreads) {
+                const int j = at / quads, col = o0 * 32 + (at - j * quads) * 4;
                 if (!sm->last[j]) continue;
                 const int t = sm->token[j];
-                const float* row = p.part + (int64_t)t * p.k * d;
+                const float* row = p.part + (int64_t)t * p.k * d + col;
                 const float* gate = p.gate + t * p.k;
-                const float* shr = p.part + ((int64_t)p.T * p.k + t) * d;
-                for (int col = o0 * 32 + pt; col < o1 * 32; col += 128) {
-                    float v[kMaxTopK];
+                const float* shr = p.part + ((int64_t)p.T * p.k + t) * d + col;
+                float4 v[kMaxTopK];
+                float g[kMaxTopK];
 #pragma unroll
-                    for (int q = 0; q < kMaxTopK; ++q) v[q] = q < p.k ? __ldcg(row + (int64_t)q * d + col) : 0.0f;
-                    float sum = __ldcg(shr + col);
-                    for (int q = 1; q < p.parts; ++q) sum += __ldcg(shr + (int64_t)q * p.T * d + col);
+                for (int q = 0; q < kMaxTopK; ++q)
+                    if (q < p.k) {
+                        v[q] = __ldcg(reinterpret_cast<const float4*>(row + (int64_t)q * d));
+                        g[q] = gate[q];
+                    }
+                float4 sum = __ldcg(reinterpret_cast<const float4*>(shr));
+                for (int q = 1; q < p.parts; ++q) {
+                    const float4 more = __ldcg(reinterpret_cast<const float4*>(shr + (int64_t)q * p.T * d));
+                    sum = make_float4(sum.x + more.x, sum.y + more.y, sum.z + more.z, sum.w + more.w);
+                }
 #pragma unroll
-                    for (int q = 0; q < kMaxTopK; ++q)
-                        if (q < p.k) sum = fmaf(gate[q], v[q], sum);
-                    if (p.y_bf16) static_cast<__nv_bfloat16*>(p.y)[(int64_t)t * d + col] = __float2bfloat16_rn(sum);
-                    else static_cast<float*>(p.y)[(int64_t)t * d + col] = sum;
+                for (int q = 0; q < kMaxTopK; ++q)
+                    if (q < p.k)
+                        sum = make_float4(fmaf(g[q], v[q].x, sum.x), fmaf(g[q], v[q].y, sum.y), fmaf(g[q], v[q].z, sum.z),
+                                          fmaf(g[q], v[q].w, sum.w));
+                const float o[4] = {sum.x, sum.y, sum.z, sum.w};
+                const int64_t to = (int64_t)t * d + col;
+                if (p.y_bf16) {
+                    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + to;
+                    if (wide) *reinterpret_cast<uint2*>(y) = make_uint2(bf16x2(o[0], o[1]), bf16x2(o[2], o[3]));
+                    else
+                        for (int i = 0; i < 4; ++i) y[i] = __float2bfloat16_rn(o[i]);
+                } else {
+                    float* y = static_cast<float*>(p.y) + to;
+                    if (wide) *reinterpret_cast<float4*>(y) = sum;
+                    else
+                        for (int i = 0; i < 4; ++i) y[i] = o[i];
                 }
             }
         }
@@ -682,17 +706,20 @@ int tile_units(int all, int S) {
 }
 
 Layout layout_for(const MoePlan& p, int S) {
-    const int hm = std::max(p.h, std::min(p.part_hidden, p.hs)), KBd = (int)blocks_of(p.d), KBh = (int)blocks_of(hm);
+    const int ph = std::min(p.part_hidden, p.hs), hm = std::max(p.h, ph), KBd = (int)blocks_of(p.d), KBh = (int)blocks_of(hm);
     Layout l = {};
     l.nu[0] = tile_units(p.h / kUnit, S);
-    l.nu[1] = tile_units(std::min(p.part_hidden, p.hs) / kUnit, S);
+    l.nu[1] = tile_units(ph / kUnit, S);
     l.no = tile_units(p.d / 32, S);
     l.hidden_ld = (hm / kUnit + S - 1) / S * kUnit;
-    const int operand = std::max(KBd, KBh) * kN * kBlk, hidden = kN * l.hidden_ld * 4;
+    const int operand = std::max(KBd, KBh) * kN * kBlk + 1024, hidden = kN * l.hidden_ld * 4;
     const int rest = operand + hidden + (KBd + KBh) * kN * 4;
-    const int half = 113 * 1024 - 2048 - 1024, whole = 226 * 1024 - 2048 - 1024;  // less static shared memory and alignment
+    // two CTAs an SM where that leaves four slots each; less static shared memory and alignment
+    const int half = 113 * 1024 - 4096, whole = 226 * 1024 - 4096;
     const int room = (half - rest) / kSlot >= 4 ? half : whole;
-    l.ring = std::min((room - rest) / kSlot, kMaxRing) / 2 * 2;
+    l.ring = std::min((room - rest) / kSlot, kMaxRing);
+    if (l.ring > 3) l.ring &= ~1;
+    l.issuers = l.ring % 2 ? 1 : 2;
     l.operand = l.ring * kSlot;
     l.hidden = l.operand + operand;
     l.sx = l.hidden + hidden;
@@ -785,10 +812,13 @@ cudaError_t launch_moe_few(const MoePlan& p, cudaStream_t st) {
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, moe_route_kernel, p);
     if (e != cudaSuccess) return e;
-    // clusters at most: the shared expert's chunks, an expert per slot, and a chunk more per 16 slots
+    // clusters: the shared expert's chunks, an expert per slot, and at most a chunk more per 8 slots.  Of 8 CTAs where
+    // all of them are on the GPU at once (two CTAs an SM), else of 4: a second round of CTAs starts with its latencies
+    // (64 tokens of 2048 features: 104 us with 8, 81 us with 4).
     const int slots = p.T * p.k;
-    const int clusters = (p.T + kN - 1) / kN * p.parts + std::min(p.E, slots) + slots / kN;
-    return launch_experts<8>(p, clusters, st);
+    const int busy = (p.T + kN - 1) / kN * p.parts + std::min(p.E, slots), clusters = busy + slots / kN;
+    if (8 * busy <= 2 * sm_count() || layout_for(p, 4).ring < 4) return launch_experts<8>(p, clusters, st);
+    return launch_experts<4>(p, clusters, st);
 }
 
 }  // namespace f8
