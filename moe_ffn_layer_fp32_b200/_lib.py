@@ -115,7 +115,7 @@ def lib() -> C.CDLL:
     L.mmoe_fp8_workspace.argtypes = [C.POINTER(Config), i64, C.POINTER(C.c_size_t)]
     L.mmoe_forward_fp8.argtypes = [C.POINTER(Config), C.POINTER(FP8Weights), vp, i64, vp, i32, vp, vp, vp, vp, C.c_size_t,
                                    vp]
-    L.mmoe_block_norm.argtypes = [C.POINTER(Norm), vp]
+    L.mmoe_block_norm.argtypes = [vp, vp]  # a Norm by reference, or its bytes
     for name in EXPORTS:
         if name != "mmoe_last_error":
             getattr(L, name).restype = st
