@@ -402,8 +402,8 @@ mmoe_status mmoe_forward_static_scratch(const mmoe_config* cfg, const mmoe_weigh
  * every buffer, on any stream, also in a stream capture, and calls on buffers
  * of their own may overlap on the GPU.  Outputs must not overlap inputs.
  * Errors of all of them: INVALID_ARG (a NULL pointer, a size, stride, type or
- * alignment out of range, overlapping buffers), CUDA, and from the products
- * TIMEOUT (a bounded wait of an earlier call on this device gave up). */
+ * alignment out of range, overlapping buffers), CUDA, and from the products and
+ * the layer TIMEOUT (a bounded wait of an earlier call on this device gave up). */
 enum { MMOE_F32 = 0, MMOE_BF16 = 1 }; /* element types of x, w and y below */
 
 /* x [rows, K] (FP32 or BF16, row stride ldx elements) to codes and scales.
@@ -447,7 +447,9 @@ mmoe_status mmoe_linear_fp8(const uint16_t* x_bf16, int64_t M, int64_t ldx, cons
  * (up Q(x)))), Q the quantisation of a row as above, silu and the products in
  * FP32, the router (FP32 weights) on x itself; the expert rows are added in
  * the order of Eq. (*), y = FFN_s + g_0 FFN_0 + ..., so that y is
- * bit-reproducible.  The config is that of mmoe_create with group_size 128 and
+ * bit-reproducible (a token's y does not depend on its batch either).  An
+ * FFN_s wider than an expert is summed in parts of ceil(h / 128) * 128 hidden
+ * features, the first part first.  The config is that of mmoe_create with group_size 128 and
  * flags 0.  All weights are device pointers, read in place (codes 16-byte
  * aligned), with KB(n) = ceil(n / 128):
  *   w_router         FP32 [d, E];  router_bias FP32 [E] or NULL

@@ -6,21 +6,25 @@
 // each block of 128 and is added in FP32 with its scales by the CUDA cores:
 // acc = fma(P_b, sa sw, acc).  One rounding, at the store of a BF16 y.
 //
-// product_kernel (many rows).  A persistent CTA per SM walks over tiles of 128
-// rows x 128 H columns (H halves of 128 weight rows).  The rows are the MMA's
-// M: each thread of the promotion warps owns one row, so a scale is one
-// register per half and block, and its 64 columns of each half stay in
-// registers.  Warps:
-//   0      producer: per block of 128 the activation tile and the H weight tiles (TMA, 128-byte swizzle)
-//   1      TMEM (two buffers of 128 H columns); one lane issues the MMAs, a commit per block
-//   2, 3   idle (they complete warpgroup 0, whose registers go to the promotion)
-//   4..11  promotion and epilogue: warp w reads TMEM lanes 32 (w % 4).. and columns 64 ((w - 4) / 4)..
-//          of each half
+// product_kernel (many rows).  Persistent CTAs, or pairs of CTAs (cta_group::2: each loads its own 128 rows and half of the
+// weight rows, so that a block of 128 brings 32 KB instead of 48 KB into an SM's shared memory), walk over tiles of C x 128
+// rows x H x 128 columns.  The rows are the MMA's M: each thread of the promotion warps owns one row, so a scale is one
+// register a block, and its columns stay in registers.  Warps:
+//   0      producer: per block of 128 the activation and the weight tile (TMA, 128-byte swizzle)
+//   1, 2   issue the MMAs, a block in turn, into 512 / (128 H) buffers of TMEM
+//   3      idle (it completes warpgroup 0, whose registers go to the promotion)
+//   4..11  promotion and epilogue: warp w reads TMEM lanes 32 (w % 4).. and half of the columns; y goes out through
+//          shared memory by the copy engine, while the next tile is on its way
+// What bounds it: the handoffs.  For 16384 x 2048 x 2048 (75 us; 1.83 PFLOP/s) a block takes about 800 clocks, of which the
+// MMAs run 515; without the additions it takes 725, without the TMEM loads 550, without the copies no less.  More buffers
+// of half the width, four promotion warps a half, FFMA2, a poll of the next buffer ahead of time and 16-byte stores by the
+// warps themselves were all slower or no faster.
 //
-// product_small_kernel (up to 64 rows).  Bound by one pass over the weights,
-// so these are the MMA's M (128 weight rows) and the few activation rows its
-// N; a cluster splits the blocks of 128 along K so that every SM streams, and
-// adds its partial sums through distributed shared memory in a fixed order.
+// product_small_kernel (up to 64 rows).  Bound by one pass over the weights and its own latencies, so these are the MMA's M
+// (128 weight rows) and the few activation rows its N; a cluster splits the blocks of 128 along K so that every SM streams,
+// and adds its partial sums through distributed shared memory in a fixed order.  1 x 2048 x 1024: 4.2 us a launch in a
+// chain (a kernel of half the shared memory: with 200 KB, which keeps the next launch off the SM, it was 7.5 us); 64 x 4096
+// x 2048: 12.9 us, 7 us of it for the codes of the rows, which every cluster makes for itself.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
