@@ -849,7 +849,7 @@ cudaError_t launch_product(const Product& p, cudaStream_t st) {
     // of 128 x 256).  Groups fill 256 rows less often (8192 rows in 60 groups: 24 us with tiles of 128 x 256, 30 us with
     // pairs; 32768 rows: 127 us and 130 us).  Where there are too few of either, tiles of 128 x 128 (777 x 1000 x 784: 9.5
     // us, 12 us with the others).
-    if (nb > 1 && !p.groups && 2 * pairs >= sm_count()) return launch_many<2, 2>(p, am, wm, pairs, st);
+    if (nb > 1 && !p.groups && p.M > kBlk && 2 * pairs >= sm_count()) return launch_many<2, 2>(p, am, wm, pairs, st);
     if (nb > 1 && singles >= sm_count()) return launch_many<1, 2>(p, am, wm, singles, st);
     return launch_many<1, 1>(p, am, wm, row_tiles(kBlk) * nb, st);
 }
