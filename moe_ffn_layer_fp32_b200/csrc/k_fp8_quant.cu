@@ -10,7 +10,7 @@ namespace f8 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kItems = 4;  // blocks a half warp holds at once: enough loads in flight to cover the latency
+constexpr int kItems = 2;  // blocks that 8 lanes hold at once: 64 bytes of BF16 a lane in flight
 
 // 8 values as they lie in memory (zeros until loaded).
 template <class T>
@@ -33,41 +33,66 @@ struct Raw8<__nv_bfloat16> {
     __device__ __forceinline__ void get(float (&o)[8]) const { unpack8(u, o); }
 };
 
-// Rows: a half warp takes one (row, block) at a time, 8 values a lane (16 bytes of BF16).
+// Rows: 8 lanes take a (row, block), 16 values a lane in two halves of 8.  Issue slots bound it beside the memory (24 us
+// for 16384 x 2048 BF16 values with 16 lanes a block, whose copy takes 16), so what is done once a block or once a thread
+// is shared: lane i of the 8 does block i's divisions, and where the rows' blocks can be counted in 32 bits they are.
 template <class T>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const T* x, int64_t nblk, int kb, int K,
                                                                  int64_t ldx, uint8_t* q,
                                                                  float* s)
 {
-    const int hl = threadIdx.x & 15;
+    constexpr int kPer = kThreads / 8 * kItems;  // blocks a CTA takes, kItems in a row 8 lanes
+    const int l = threadIdx.x & 7;
+    const int64_t first = (int64_t)blockIdx.x * kPer + (threadIdx.x >> 3) * kItems;
+    const int64_t row = nblk < (int64_t(1) << 31) ? (int64_t)((uint32_t)first / (uint32_t)kb) : first / kb;
+    int col = (int)(first - row * kb) * kBlk + l * 8;
+    const T* from = x + row * ldx + col;
+    uint8_t* to = q + row * K + col;
     dep_launch();
     dep_wait();
-    constexpr int kPer = kThreads / 16 * kItems;  // blocks a CTA takes, kItems in a row a half warp
-    const int64_t begin = (int64_t)blockIdx.x * kPer, row0 = begin / kb;
-    const int b0 = (int)(begin - row0 * kb), mine = (threadIdx.x >> 4) * kItems;
-    const int64_t first = begin + mine;
-    Raw8<T> v[kItems];
-    int64_t at[kItems];  // of the lane's values in q (-1: none)
-    int64_t row = row0 + (b0 + mine) / kb;  // 64-bit divisions for each block took three times the copy's time
-    int col = (b0 + mine) % kb * kBlk + hl * 8;
+    Raw8<T> v[kItems][2];
+    uint8_t* at[kItems][2];  // where the lane's codes go (null: nowhere)
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-        const bool in = first + i < nblk && col < K;
-        at[i] = in ? row * K + col : -1;
-        if (in) v[i].load(x + row * ldx + col);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            at[i][h] = nullptr;
+            if (first + i < nblk && col + 64 * h < K) {
+                v[i][h].load(from + 64 * h);
+                at[i][h] = to + 64 * h;
+            }
+        }
         col += kBlk;
-        if (col >= kb * kBlk) {
-            col = hl * 8;
-            ++row;
+        from += kBlk;
+        to += kBlk;
+        if (col >= kb * kBlk) {  // on to the next row
+            col -= kb * kBlk;
+            from += ldx - (int64_t)kb * kBlk;
+            to += K - kb * kBlk;
         }
     }
-    float sc[kItems];
-    uint2 code[kItems];
-    encode<kItems>(kItems, [&](int i) { return v[i].amax(); }, [&](int i, float (&o)[8]) { v[i].get(o); }, sc, code);
+    uint32_t m[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) m[i] = max(v[i][0].amax(), v[i][1].amax());
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+    uint32_t mine = m[0];
+#pragma unroll
+    for (int i = 1; i < kItems; ++i)
+        if ((threadIdx.x & (kItems - 1)) == i) mine = m[i];
+    const float scale = scale_of(mine), inv = Coder::inverse(scale);
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-        if (hl == 0 && first + i < nblk) s[first + i] = sc[i];
-        if (at[i] >= 0) *reinterpret_cast<uint2*>(q + at[i]) = code[i];
+        const Coder code(__shfl_sync(0xffffffffu, scale, i, 8), __shfl_sync(0xffffffffu, inv, i, 8));
+        if (l == 0 && first + i < nblk) s[first + i] = code.s;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float o[8];
+            v[i][h].get(o);
+            if (at[i][h]) *reinterpret_cast<uint2*>(at[i][h]) = code(o);
+        }
     }
 }
 
@@ -129,7 +154,7 @@ cudaLaunchConfig_t dependent(unsigned grid, cudaStream_t st, cudaLaunchAttribute
 
 cudaError_t launch_quantize_rows(const void* x, bool bf16, int64_t rows, int64_t K, int64_t ldx, uint8_t* q, float* s,
                                  cudaStream_t st) {
-    const int64_t kb = blocks_of(K), nblk = rows * kb, per = kThreads / 16 * kItems;
+    const int64_t kb = blocks_of(K), nblk = rows * kb, per = kThreads / 8 * kItems;
     cudaLaunchAttribute at;
     const cudaLaunchConfig_t cfg = dependent((unsigned)((nblk + per - 1) / per), st, &at);
     return bf16 ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<__nv_bfloat16>, (const __nv_bfloat16*)x, nblk, (int)kb,
