@@ -135,16 +135,16 @@ __device__ __forceinline__ uint32_t amax_bf16(const uint4& u) {
     return max(m << 16, m & 0xffff0000u);
 }
 
-// Scales and codes of the first n of U blocks, 16 lanes (8 values each) a block: peak(u) gives a lane's largest
-// magnitude, get(u, values) the values.  All blocks side by side, for one after the other each waits for its own
-// maximum, divisions and conversions; lane u of the 16 does block u's divisions.
+// Scales and codes of the first n of U blocks, 8 lanes a block with 16 values each in two halves: peak(u) gives a lane's
+// largest magnitude, get(u, half, values) the values.  All blocks side by side, for one after the other each waits for its
+// own maximum, divisions and conversions; lane u of the 8 does block u's divisions.
 template <int U, class Peak, class Get>
-__device__ __forceinline__ void encode(int n, const Peak& peak, const Get& get, float (&s)[U], uint2 (&q)[U]) {
+__device__ __forceinline__ void encode(int n, const Peak& peak, const Get& get, float (&s)[U], uint2 (&q)[U][2]) {
     uint32_t m[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) m[u] = u < n ? peak(u) : 0u;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1)
+    for (int o = 4; o > 0; o >>= 1)
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (u < n) m[u] = max(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
@@ -156,10 +156,14 @@ __device__ __forceinline__ void encode(int n, const Peak& peak, const Get& get, 
 #pragma unroll
     for (int u = 0; u < U; ++u)
         if (u < n) {
-            float v[8];
-            get(u, v);
-            s[u] = __shfl_sync(0xffffffffu, scale, u, 16);
-            q[u] = Coder(s[u], __shfl_sync(0xffffffffu, inv, u, 16))(v);
+            s[u] = __shfl_sync(0xffffffffu, scale, u, 8);
+            const Coder code(s[u], __shfl_sync(0xffffffffu, inv, u, 8));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v[8];
+                get(u, h, v);
+                q[u][h] = code(v);
+            }
         }
 }
 

@@ -541,52 +541,59 @@ struct SmallSmem {
     int abort;
 };
 
-// Codes and scales of the activation rows of n blocks of K, those of this CTA from its i0-th on, into the operand buffer: a
-// half warp per (row, block).
+// Codes and scales of the activation rows of n blocks of K, those of this CTA from its i0-th on, into the operand buffer: 8
+// lanes per (row, block), 16 values a lane.
 template <int NT>
 __device__ __forceinline__ void encode_rows(const Product& p, SmallSmem<NT>* sm, int rank, int C, int KB, int i0, int n, int pt) {
-    constexpr int kBatch = NT == 16 ? 2 : 4;      // items in flight a half warp
-    constexpr int kStep = 2 * quant_warps<NT>();  // half warps
-    const int m = (int)p.M, hl = pt & 15;
+    constexpr int kBatch = NT == 16 ? 1 : 2;      // items in flight of 8 lanes
+    constexpr int kStep = 4 * quant_warps<NT>();  // such groups of 8 lanes
+    const int m = (int)p.M, l = pt & 7;
     const float inv = __fdividef(1.0f, (float)m);
-    // (both half warps of a warp make the same turns: they meet in the shuffles)
-    for (int jw = pt >> 5 << 1; jw < n * m; jw += kStep * kBatch) {
-        const int j0 = jw + (pt >> 4 & 1);
-        uint4 raw[kBatch] = {};
+    // (the four groups of a warp make the same turns: they meet in the shuffles)
+    for (int jw = pt >> 5 << 2; jw < n * m; jw += kStep * kBatch) {
+        const int j0 = jw + (pt >> 3 & 3);
+        uint4 raw[kBatch][2] = {};
         float sc[kBatch];
-        uint2 code[kBatch];
+        uint2 code[kBatch][2];
         int at[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             if (jw + kStep * u >= n * m) continue;
-            const int j = min(j0 + kStep * u, n * m - 1);                 // the last one may be read by both
+            const int j = min(j0 + kStep * u, n * m - 1);                 // the last one may be read by several
             const int r = (int)(((float)j + 0.5f) * inv), t = j - r * m;  // exact: j is below 2^12
-            const int kb = rank + (i0 + r) * C, col = kb * kBlk + hl * 8;
+            const int kb = rank + (i0 + r) * C;
             at[u] = r * NT + t;
-            if (p.x) {
-                if (col < p.K) raw[u] = *reinterpret_cast<const uint4*>(p.x + t * p.ldx + col);
-            } else {
-                if (col < p.K) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int col = kb * kBlk + h * 64 + l * 8;
+                if (col >= p.K) continue;
+                if (p.x) {
+                    raw[u][h] = *reinterpret_cast<const uint4*>(p.x + t * p.ldx + col);
+                } else {
                     const uint2 q = *reinterpret_cast<const uint2*>(p.a + (int64_t)t * p.K + col);
-                    raw[u].x = q.x;
-                    raw[u].y = q.y;
+                    raw[u][h].x = q.x;
+                    raw[u][h].y = q.y;
                 }
-                sc[u] = p.sa[(int64_t)t * KB + kb];
             }
+            if (!p.x) sc[u] = p.sa[(int64_t)t * KB + kb];
         }
         if (p.x) {
-            encode<kBatch>((n * m - jw + kStep - 1) / kStep, [&](int u) { return amax_bf16(raw[u]); },
-                           [&](int u, float (&v)[8]) { unpack8(raw[u], v); }, sc, code);
+            encode<kBatch>((n * m - jw + kStep - 1) / kStep, [&](int u) { return max(amax_bf16(raw[u][0]), amax_bf16(raw[u][1])); },
+                           [&](int u, int h, float (&v)[8]) { unpack8(raw[u][h], v); }, sc, code);
         } else {
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) code[u] = make_uint2(raw[u].x, raw[u].y);
+            for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) code[u][h] = make_uint2(raw[u][h].x, raw[u][h].y);
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             if (jw + kStep * u >= n * m) continue;
-            if (hl == 0) (&sm->sx[0][0])[at[u]] = sc[u];
+            if (l == 0) (&sm->sx[0][0])[at[u]] = sc[u];
             // 128-byte swizzle: 16-byte chunk c of row t lies at chunk c ^ (t & 7) (NT is a multiple of 8)
-            *reinterpret_cast<uint2*>(sm->b + at[u] * kBlk + (((hl >> 1) ^ (at[u] & 7)) << 4) + (hl & 1) * 8) = code[u];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<uint2*>(sm->b + at[u] * kBlk + (((4 * h + (l >> 1)) ^ (at[u] & 7)) << 4) + (l & 1) * 8) = code[u][h];
         }
     }
     fence_async_smem();

@@ -35,7 +35,7 @@ struct Raw8<__nv_bfloat16> {
 
 // Rows: 8 lanes take a (row, block), 16 values a lane in two halves of 8.  Issue slots bound it beside the memory (24 us
 // for 16384 x 2048 BF16 values with 16 lanes a block, whose copy takes 16), so what is done once a block or once a thread
-// is shared: lane i of the 8 does block i's divisions, and where the rows' blocks can be counted in 32 bits they are.
+// is shared, and where the rows' blocks can be counted in 32 bits they are.
 template <class T>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const T* x, int64_t nblk, int kb, int K,
                                                                  int64_t ldx, uint8_t* q,
@@ -71,28 +71,16 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const T* x, int
             to += K - kb * kBlk;
         }
     }
-    uint32_t m[kItems];
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) m[i] = max(v[i][0].amax(), v[i][1].amax());
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < kItems; ++i) m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
-    uint32_t mine = m[0];
-#pragma unroll
-    for (int i = 1; i < kItems; ++i)
-        if ((threadIdx.x & (kItems - 1)) == i) mine = m[i];
-    const float scale = scale_of(mine), inv = Coder::inverse(scale);
+    float sc[kItems];
+    uint2 code[kItems][2];
+    encode<kItems>(kItems, [&](int i) { return max(v[i][0].amax(), v[i][1].amax()); },
+                   [&](int i, int h, float (&o)[8]) { v[i][h].get(o); }, sc, code);
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-        const Coder code(__shfl_sync(0xffffffffu, scale, i, 8), __shfl_sync(0xffffffffu, inv, i, 8));
-        if (l == 0 && first + i < nblk) s[first + i] = code.s;
+        if (l == 0 && first + i < nblk) s[first + i] = sc[i];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float o[8];
-            v[i][h].get(o);
-            if (at[i][h]) *reinterpret_cast<uint2*>(at[i][h]) = code(o);
-        }
+        for (int h = 0; h < 2; ++h)
+            if (at[i][h]) *reinterpret_cast<uint2*>(at[i][h]) = code[i][h];
     }
 }
 
