@@ -73,7 +73,7 @@ static __device__ __noinline__ uint32_t divided4(float a, float b, float c, floa
 // (16 either way) every V was checked on the CPU: always the IEEE quotient.  A code that is not 0 needs v >= s 2^-11, and
 // the remainder is a multiple of v 2^-47, which must not underflow; blocks outside that range, of zeros, with NaN or
 // infinities are divided.  (Bounding the quotient from both sides by two products costs less, but BF16 values lie on a
-// border too often: one in 200.)  Quantising 32768 x 2048 BF16 values took 106 us with a division each, and takes 45 us.
+// border too often: one in 200.)  Quantising 32768 x 2048 BF16 values took 106 us with a division each, and takes 39 us.
 struct Coder {
     float s, y;
     bool fast;
@@ -359,19 +359,6 @@ __device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b
     const bool first = async::mbar_try_wait(a, pa), both = async::mbar_try_wait(b, pb) && first;
     if (__all_sync(0xffffffffu, both)) return true;
     return warp_wait(a, pa, abort_word, err, site) && warp_wait(b, pb, abort_word, err, site);
-}
-
-// Whether the phase is complete, without waiting for it (mbar_try_wait may hold the thread for a while).
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(async::su32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
 }
 
 // One lane of a converged warp, the same each time.

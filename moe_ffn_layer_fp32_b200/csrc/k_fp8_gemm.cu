@@ -22,9 +22,9 @@
 //
 // product_small_kernel (up to 64 rows).  Bound by one pass over the weights and its own latencies, so these are the MMA's M
 // (128 weight rows) and the few activation rows its N; a cluster splits the blocks of 128 along K so that every SM streams,
-// and adds its partial sums through distributed shared memory in a fixed order.  1 x 2048 x 1024: 4.2 us a launch in a
-// chain (a kernel of half the shared memory: with 200 KB, which keeps the next launch off the SM, it was 7.5 us); 64 x 4096
-// x 2048: 12.9 us, 7 us of it for the codes of the rows, which every cluster makes for itself.
+// and adds its partial sums through distributed shared memory in a fixed order.  1 x 2048 x 1024: 3.6 us a launch in a
+// chain (with 200 KB of shared memory instead of half, which keeps the next launch off the SM, 7.5 us); 64 x 4096 x 2048: 11.0
+// us, half of it for the codes of the rows, which every cluster makes for itself.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -852,8 +852,8 @@ cudaError_t launch_product(const Product& p, cudaStream_t st) {
     const int64_t nb = blocks_of(p.N), wide = (nb + 1) / 2, pairs = row_tiles(2 * kBlk) * wide, singles = row_tiles(kBlk) * wide;
     e = byte_map(&wm, p.w, (uint64_t)p.K, (uint64_t)(G * p.N), (uint64_t)p.K, kBlk);
     if (e != cudaSuccess) return e;
-    // Dense rows go to pairs of CTAs where there are tiles for all of them (32768 x 2048 x 2048: 221 us, 232 us with tiles
-    // of 128 x 256).  Groups fill 256 rows less often (8192 rows in 60 groups: 24 us with tiles of 128 x 256, 30 us with
+    // Dense rows go to pairs of CTAs where there are tiles for all of them (32768 x 2048 x 2048 with its quantisation: 221 us,
+    // 232 us with tiles of 128 x 256).  Groups fill 256 rows less often (8192 rows in 60 groups: 24 us with tiles of 128 x 256, 30 us with
     // pairs; 32768 rows: 127 us and 130 us).  Where there are too few of either, tiles of 128 x 128 (777 x 1000 x 784: 9.5
     // us, 12 us with the others).
     if (nb > 1 && !p.groups && p.M > kBlk && 2 * pairs >= sm_count()) return launch_many<2, 2>(p, am, wm, pairs, st);
