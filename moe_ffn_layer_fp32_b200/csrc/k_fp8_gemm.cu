@@ -103,7 +103,6 @@ constexpr int kThreads = 128 + 32 * kPromoWarps;
 // Register split (setmaxnreg): 168 a thread at launch; warpgroup 0 drops to 40, the promotion rises to 232.
 constexpr int kRegsLow = 40, kRegsHigh = 232;
 static_assert(128 * kRegsLow + 32 * kPromoWarps * kRegsHigh <= kThreads * 168, "register split");
-constexpr int kOutBytes = 8192;          // staging of a promotion warp: 32 rows x 128 bytes, once or twice
 
 struct TileInfo {
     int end;
@@ -118,60 +117,63 @@ struct TileInfo {
 template <int C, int H>
 struct Smem {
     static constexpr int kWeights = H / C * kTileBytes;            // of a block of K, in a CTA
+    // (Four stages and two issuers of 128 x 256, with half the staging, are faster in short runs, 103 us instead of 110 for
+    // 32768 expert rows, and slower under the power cap, 133 us instead of 129.)
     static constexpr int kStages = H > C ? 3 : 4;
+    static constexpr int kOut = 8192;                              // staging of a promotion warp: 32 rows x 128 bytes, once or twice
     alignas(1024) uint8_t ring[kStages][kTileBytes + kWeights];    // 128 activation rows, the weight rows
-    alignas(1024) uint8_t out[kPromoWarps][kOutBytes];
+    alignas(1024) uint8_t out[kPromoWarps][kOut];
     uint64_t full[kStages], empty[kStages];
     uint64_t accf[kMaxBufs], acce[kMaxBufs];
     uint64_t tfull[kTInfo], tempty[kTInfo];
     TileInfo ti[kTInfo];
     uint32_t tmem;
     int abort;
-    int off[kMaxGroups + 1];     // grouped: first row of each group
-    int tiles[kMaxGroups + 1];   // grouped: row tiles before each group
 };
 
-// Offsets of the groups, made harmless: within [0, M] and not decreasing, whatever the array holds.
-// Warp 0 of the CTA; 32 groups a step.
-template <int C, int H>
-__device__ __forceinline__ void load_groups(const Product& p, Smem<C, H>* sm, int lane) {
-    constexpr int kRows = C * kBlk;
-    int prev = 0, base = 0;
-    for (int g0 = 0; g0 < p.groups; g0 += 32) {
+// Walks over the groups of a grouped product in a warp's registers, 32 groups at a time (a lane a group).  The offsets are
+// made harmless on the way: within [0, M] and not decreasing, whatever the array holds.
+template <int kRows>
+struct Groups {
+    int g0 = -32, prev = 0, end = 0;  // first group held, first row behind them, tiles up to there
+    int first = 0, last = 0, tiles = 0, upto = 0;  // of the lane's group: rows [first, last), tiles, tiles up to its last
+
+    __device__ __forceinline__ void next(const Product& p, int lane) {
+        if (g0 < 0) prev = min(max(p.offsets[0], 0), (int)p.M);
+        g0 += 32;
         const int g = g0 + lane;
-        int o = g < p.groups ? p.offsets[g + 1] : 0;
-        if (g0 == 0) {
-            int first = p.offsets[0];
-            first = min(max(first, 0), (int)p.M);
-            prev = first;
-            if (lane == 0) {
-                sm->off[0] = first;
-                sm->tiles[0] = 0;
-            }
-        }
-        o = min(max(o, prev), (int)p.M);
+        last = min(max(g < p.groups ? p.offsets[g + 1] : 0, prev), (int)p.M);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, o, d);
-            if (lane >= d) o = max(o, u);
+            const int u = __shfl_up_sync(0xffffffffu, last, d);
+            if (lane >= d) last = max(last, u);
         }
-        int before = __shfl_up_sync(0xffffffffu, o, 1);
-        if (lane == 0) before = prev;
-        int t = g < p.groups ? (o - before + kRows - 1) / kRows : 0;
+        first = __shfl_up_sync(0xffffffffu, last, 1);
+        if (lane == 0) first = prev;
+        tiles = g < p.groups ? (last - first + kRows - 1) / kRows : 0;
+        upto = tiles;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, t, d);
-            if (lane >= d) t += u;
+            const int u = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += u;
         }
-        if (g < p.groups) {
-            sm->off[g + 1] = o;
-            sm->tiles[g + 1] = base + t;
-        }
-        prev = __shfl_sync(0xffffffffu, o, 31);
-        base += __shfl_sync(0xffffffffu, t, 31);
+        upto += end;
+        prev = __shfl_sync(0xffffffffu, last, 31);
+        end = __shfl_sync(0xffffffffu, upto, 31);
     }
-    __syncwarp();
-}
+    // Row tile mt (not below an earlier one): its group and rows; false behind the last.
+    __device__ __forceinline__ bool find(const Product& p, int lane, int64_t mt, int& g, int64_t& row0, int64_t& rows) {
+        while (mt >= end) {
+            if (g0 + 32 >= p.groups) return false;
+            next(p, lane);
+        }
+        const int at = __ffs(__ballot_sync(0xffffffffu, upto > mt)) - 1;
+        g = g0 + at;
+        row0 = __shfl_sync(0xffffffffu, first, at) + (mt - __shfl_sync(0xffffffffu, upto - tiles, at)) * kRows;
+        rows = __shfl_sync(0xffffffffu, last, at);
+        return true;
+    }
+};
 
 // A box of the staging buffer: 32 rows of 128 bytes, 16-byte chunk c of row r at chunk c ^ (r & 7) (the 128-byte
 // swizzle of the copy engine, and no bank conflict).  The thread that owns row r writes it from its accumulators ...
@@ -264,41 +266,25 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         if (warp == 0) {
-            int64_t total;
-            if (p.groups) {
-                load_groups<C, H>(p, sm, lane);
-                total = (int64_t)sm->tiles[p.groups] * ntiles;
-            } else {
-                total = (p.M + kRows - 1) / kRows * ntiles;
-            }
+            const int64_t total = (p.M + kRows - 1) / kRows * ntiles;  // of a dense product
+            Groups<kRows> groups;
             int sc = 0, tc = 0;
             bool ok = true;
             for (int64_t L = blockIdx.x / C; ok; L += gridDim.x / C, ++tc) {
                 const int b = tc % kTInfo;
                 if (tc >= kTInfo && !warp_wait(&sm->tempty[b], (tc / kTInfo - 1) & 1, &sm->abort, p.err, 1)) break;
                 TileInfo& ti = sm->ti[b];
-                if (L >= total) {
-                    if (lane == 0) {
-                        ti.end = 1;
-                        mbar_arrive(&sm->tfull[b]);
-                    }
-                    break;
-                }
                 // column tiles innermost: the CTAs that run together share activation tiles in L2
                 const int64_t mt = L / ntiles;
                 const int nt = (int)(L - mt * ntiles);
                 int g = 0;
                 int64_t row0 = mt * kRows, rows = p.M;
-                if (p.groups) {
-                    int lo = 0, hi = p.groups - 1;  // the last group with tiles[g] <= mt
-                    while (lo < hi) {
-                        const int mid = (lo + hi + 1) >> 1;
-                        if (sm->tiles[mid] <= mt) lo = mid;
-                        else hi = mid - 1;
+                if (p.groups ? !groups.find(p, lane, mt, g, row0, rows) : L >= total) {
+                    if (lane == 0) {
+                        ti.end = 1;
+                        mbar_arrive(&sm->tfull[b]);
                     }
-                    g = lo;
-                    row0 = sm->off[g] + (mt - sm->tiles[g]) * kRows;
-                    rows = sm->off[g + 1];
+                    break;
                 }
                 const int n0 = nt * H * kBlk;
                 // CTA 1 of a pair may have no rows: then it loads none, and its half of the product is not used
@@ -343,8 +329,8 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                 for (int i = max(sc - S, 0); i < sc; ++i) wait_drain(&sm->full[i % S], (i / S) & 1);
         } else if (warp <= kIssuers) {
             // Two warps issue in turn, a block of K each: its MMAs run for 515 clocks (a pair) or 288, but what one warp
-            // does for it (two waits, four MMAs, two commits) takes about 600.  (The MMAs of a single CTA's wide tile
-            // wait for shared memory longer than that: one warp.)  A warp walks together and one lane issues: in a
+            // does for it (two waits, four MMAs, two commits) takes about 600.  (The MMAs of a single CTA's wide tile wait
+            // for shared memory longer than that: one warp.)  A warp walks together and one lane issues: in a
             // branch of one lane the same loop takes half as long again.  Each warp keeps to its own buffers and ring
             // stages, so that no phase of a barrier passes unseen.
             static_assert(S % kIssuers == 0 && kBufs % kIssuers == 0, "ownership");
@@ -471,7 +457,7 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
             }
             if (!ok || __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&sm->abort))) break;
             constexpr int kBox = 128 / (int)sizeof(T);           // columns of a box
-            constexpr int kRound = kOutBytes / (32 * 128);       // boxes staged at once
+            constexpr int kRound = Sm::kOut / (32 * 128);        // boxes staged at once
             const int64_t y0 = ti.row0 + quarter * 32;
             const int nr = min(ti.nr - quarter * 32, 32), n0 = ti.n0 + set * kCols;
             more = next();

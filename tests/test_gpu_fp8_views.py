@@ -85,3 +85,26 @@ def test_wide_shared_expert_in_many_parts(fp8):
     c = moe.Case(64, 32, 1056, 4, 1, seed=14)
     x = c.x(19)
     c.check(x, *moe.forward(c.layer(fp8), c, x))
+
+
+@pytest.mark.parametrize("n", [40, 1200])
+def test_many_groups(fp8, n):
+    """1024 groups, most of them empty or of a row or two, a few offsets that go back; each a small product of its own."""
+    k, G = 16, 1024
+    counts = torch.randint(0, 4, (G,), generator=gen(15)) * (torch.rand(G, generator=gen(16)) < 0.4)
+    counts[100:300] = 0
+    counts[511], counts[512], counts[1023] = 140, 0, 5
+    off = torch.cat([torch.zeros(1, dtype=torch.long), counts.cumsum(0)])
+    m = int(off[-1])
+    given = off.clone()
+    given[150], given[200], given[250] = 0, -9, 3  # inside an empty stretch: taken as what is before them
+    xq, xs = U.quantize_rows(activations(m, k, 17))
+    wq = torch.randn(G, n, k, generator=gen(18)).to(torch.float8_e4m3fn)
+    ws = torch.rand(G, -(-n // 128), 1, generator=gen(19))
+    y = fp8.grouped_gemm_fp8(codes(xq), xs.cuda(), given.int().cuda(), wq.cuda(), ws.cuda(), out_dtype=F32)
+    a = U.values_rows(xq, xs)
+    of = torch.searchsorted(off[1:], torch.arange(m), right=True)
+    w = wq.double() * ws.double().repeat_interleave(128, 1)[:, :n]
+    ref = torch.einsum("mk,mnk->mn", a, w[of])
+    size = torch.einsum("mk,mnk->mn", a.abs(), w[of].abs())
+    U.assert_within(y, ref, size * (128 * 2 + 11) * 2.0 ** -24 + 2.0 ** -120, F32)
