@@ -263,8 +263,9 @@ mmoe_status mmoe_linear_fp8(const uint16_t* x_bf16, int64_t M, int64_t ldx, cons
     if (!workspace || !aligned16(workspace) || workspace_bytes < need)
         return report(MMOE_ERR_INVALID_ARG, "the workspace must be 16-byte aligned and %zu bytes long", need);
     if (overlap(workspace, (int64_t)need, y, yb) || overlap(workspace, (int64_t)need, x_bf16, xb) ||
-        overlap(workspace, (int64_t)need, w, N * K))
-        return report(MMOE_ERR_INVALID_ARG, "the workspace overlaps x, y or the weights");
+        overlap(workspace, (int64_t)need, w, N * K) ||
+        overlap(workspace, (int64_t)need, sw, f8::blocks_of(N) * f8::blocks_of(K) * 4))
+        return report(MMOE_ERR_INVALID_ARG, "the workspace overlaps x, y, the weights or their scales");
     CHECK(device_flag(&p.err));
     float* s = static_cast<float*>(workspace);
     uint8_t* q = static_cast<uint8_t*>(workspace) + scale_bytes(M, K);
