@@ -63,6 +63,7 @@ int64_t size_of(int32_t t) { return t == MMOE_BF16 ? 2 : 4; }
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 256;
 constexpr int64_t kMaxDim = 1 << 20;
 constexpr int64_t kMaxStride = int64_t(1) << 36;  // elements; the copy engine takes less than 2^40 bytes
+constexpr int64_t kMaxSpan = int64_t(1) << 48;    // elements from the first row of a tensor to its last: more than an address space
 
 mmoe_status check_dim(int64_t v, const char* what, int64_t step) {
     if (v < step || v > kMaxDim || v % step)
@@ -73,6 +74,13 @@ mmoe_status check_dim(int64_t v, const char* what, int64_t step) {
 
 mmoe_status check_rows(int64_t v, const char* what) {
     if (v < 0 || v > kMaxRows) return report(MMOE_ERR_INVALID_ARG, "%s=%lld: must be in [0, 2^31 - 256]", what, (long long)v);
+    return MMOE_OK;
+}
+
+// So that (rows - 1) * ld, and the bytes computed from it, are far from 2^63.
+mmoe_status check_span(int64_t rows, int64_t ld, const char* what) {
+    if (ld > 0 && rows - 1 > kMaxSpan / ld)
+        return report(MMOE_ERR_INVALID_ARG, "%lld rows %s=%lld elements apart span more than 2^48", (long long)rows, what, (long long)ld);
     return MMOE_OK;
 }
 
@@ -91,6 +99,7 @@ mmoe_status check_product(int64_t M, const uint8_t* w, const float* sw, int64_t 
     CHECK(check_type(y_type, "y_type"));
     if (ldy < N || ldy > kMaxStride)
         return report(MMOE_ERR_INVALID_ARG, "ldy=%lld: must be at least N=%lld and at most 2^36", (long long)ldy, (long long)N);
+    CHECK(check_span(M, ldy, "ldy"));
     if (G * N > kMaxRows || G * f8::blocks_of(N) * f8::blocks_of(K) > kMaxRows)
         return report(MMOE_ERR_INVALID_ARG, "the weights have too many rows or blocks");
     if (M == 0) return MMOE_OK;
@@ -172,6 +181,7 @@ mmoe_status mmoe_quantize_fp8_rows(const void* x, int32_t x_type, int64_t rows, 
     const int64_t es = size_of(x_type), kb = f8::blocks_of(K);
     if (ldx < K || ldx % (16 / es) || ldx > kMaxStride)
         return report(MMOE_ERR_INVALID_ARG, "ldx=%lld: must be at least K, at most 2^36 and whole 16 bytes", (long long)ldx);
+    CHECK(check_span(rows, ldx, "ldx"));
     if (rows == 0) return MMOE_OK;
     if (rows * kb > (int64_t(1) << 36)) return report(MMOE_ERR_INVALID_ARG, "too many blocks");
     if (!x || !q || !s) return report(MMOE_ERR_INVALID_ARG, "a pointer is NULL");
@@ -191,8 +201,9 @@ mmoe_status mmoe_quantize_fp8_blocks(const void* w, int32_t w_type, int64_t batc
     CHECK(check_dim(K, "K", 8));
     CHECK(check_type(w_type, "w_type"));
     if (batch == 0) return MMOE_OK;
-    const int64_t es = size_of(w_type), nblk = batch * f8::blocks_of(N) * f8::blocks_of(K), n = batch * N * K;
+    const int64_t es = size_of(w_type), nblk = batch * f8::blocks_of(N) * f8::blocks_of(K);
     if (nblk > kMaxRows) return report(MMOE_ERR_INVALID_ARG, "too many blocks");
+    const int64_t n = batch * N * K;
     if (!w || !q || !s) return report(MMOE_ERR_INVALID_ARG, "a pointer is NULL");
     if (!aligned16(w) || reinterpret_cast<uintptr_t>(q) % 8 || reinterpret_cast<uintptr_t>(s) % 4)
         return report(MMOE_ERR_INVALID_ARG, "w must be 16-byte, q 8-byte and s 4-byte aligned");
@@ -247,6 +258,7 @@ mmoe_status mmoe_linear_fp8(const uint16_t* x_bf16, int64_t M, int64_t ldx, cons
     CHECK(check_product(M, w, sw, 1, N, K, y, y_type, ldy));
     if (ldx < K || ldx % 8 || ldx > kMaxStride)
         return report(MMOE_ERR_INVALID_ARG, "ldx=%lld: must be at least K, at most 2^36 and a multiple of 8", (long long)ldx);
+    CHECK(check_span(M, ldx, "ldx"));
     if (M == 0) return MMOE_OK;
     if (!x_bf16 || !aligned16(x_bf16)) return report(MMOE_ERR_INVALID_ARG, "x is NULL or not 16-byte aligned");
     const int64_t xb = ((M - 1) * ldx + K) * 2, yb = ((M - 1) * ldy + N) * size_of(y_type);
@@ -370,11 +382,13 @@ mmoe_status mmoe_block_norm(const mmoe_norm* n, void* stream) {
         if (!t.p) continue;
         if (t.ld < d || t.ld % (16 / t.size) || t.ld > kMaxStride || !aligned16(t.p))
             return report(MMOE_ERR_INVALID_ARG, "%s must be 16-byte aligned with rows of at least d elements and whole 16 bytes apart", t.name);
+        CHECK(check_span(rows, t.ld, t.name));
     }
     if (n->gate && (n->gate_col != 0 && n->gate_col != 1))
         return report(MMOE_ERR_INVALID_ARG, "gate_col=%d: must be 0 or 1", n->gate_col);
     if (n->gate && (n->gate_row < 0 || n->gate_row > kMaxStride))
         return report(MMOE_ERR_INVALID_ARG, "gate_row must be in [0, 2^36]");
+    if (n->gate) CHECK(check_span(rows, n->gate_row, "gate_row"));
     if (n->gate && (n->gate_col ? (!aligned16(n->gate) || n->gate_row % 4) : reinterpret_cast<uintptr_t>(n->gate) % 4 != 0))
         return report(MMOE_ERR_INVALID_ARG, "gate: a gate per feature needs 16-byte aligned rows, one per row 4-byte ones");
     for (const void* p : {(const void*)n->w_post, (const void*)n->w_pre, (const void*)n->x, (const void*)n->xq})
