@@ -403,7 +403,10 @@ mmoe_status mmoe_forward_static_scratch(const mmoe_config* cfg, const mmoe_weigh
  * of their own may overlap on the GPU.  Outputs must not overlap inputs.
  * Errors of all of them: INVALID_ARG (a NULL pointer, a size, stride, type or
  * alignment out of range, overlapping buffers), CUDA, and from the products and
- * the layer TIMEOUT (a bounded wait of an earlier call on this device gave up). */
+ * the layer TIMEOUT: a bounded wait of an earlier product or layer call on this
+ * device gave up (after about 2 s; that call's outputs are undefined).  It is
+ * reported once, by whichever of these calls comes next, which then does
+ * nothing, or by mmoe_fp8_status. */
 enum { MMOE_F32 = 0, MMOE_BF16 = 1 }; /* element types of x, w and y below */
 
 /* x [rows, K] (FP32 or BF16, row stride ldx elements) to codes and scales.
@@ -480,6 +483,23 @@ mmoe_status mmoe_fp8_workspace(const mmoe_config* cfg, int64_t T, size_t* bytes)
 mmoe_status mmoe_forward_fp8(const mmoe_config* cfg, const mmoe_fp8_weights* w, const uint16_t* x_bf16, int64_t T, void* y,
                              int32_t y_type, int32_t* topk_idx, float* topk_gate, int32_t* expert_counts,
                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Reports, once, with MMOE_ERR_TIMEOUT that a bounded wait of a product or layer
+ * call on the current device has given up, and MMOE_OK otherwise.  Launches
+ * nothing and waits for nothing: it knows of work that has ended (synchronise
+ * first).  For replays of captured graphs, which no call reports, and after the
+ * last call of a program.  Errors: TIMEOUT, CUDA. */
+mmoe_status mmoe_fp8_status(void);
+
+/* Failure detection without a GPU fault, as mmoe_debug_set_wait_limit: from now
+ * on the bounded waits of the products and the layer, on every device, last
+ * `clocks` SM clocks (0: the default, about 4e9).  With stall_next = 1 or 2 the
+ * next one of these calls makes one CTA of its kernel wait for a barrier that
+ * nothing signals: 1 those of its warps that issue the matrix instructions, 2
+ * those that add up what they produce, in the last CTA of the first cluster
+ * or pair.  A captured call keeps both values in its graph.  A caller has no reason to call this
+ * outside tests.  Errors: INVALID_ARG (clocks < 0, stall_next not 0, 1 or 2). */
+mmoe_status mmoe_debug_fp8_waits(int64_t clocks, int32_t stall_next);
 
 /* ---- between two blocks -----------------------------------------------------
  * The norm after a block, the block's gate, the residual update and the norm

@@ -35,7 +35,7 @@ EXPORTS = ("mmoe_create", "mmoe_load_quantized_weights", "mmoe_forward", "mmoe_f
            "mmoe_debug_set_wait_limit", "mmoe_debug_fail_alloc", "mmoe_forward_chain",
            "mmoe_quantize_fp8_rows", "mmoe_quantize_fp8_blocks", "mmoe_gemm_fp8", "mmoe_gemm_fp8_grouped",
            "mmoe_linear_fp8_workspace", "mmoe_linear_fp8", "mmoe_fp8_workspace", "mmoe_forward_fp8",
-           "mmoe_block_norm")
+           "mmoe_fp8_status", "mmoe_debug_fp8_waits", "mmoe_block_norm")
 MAX_CHAIN_LAYERS = 32
 
 F32, BF16 = 0, 1  # element types of the e4m3 operators and the block norm
@@ -115,6 +115,8 @@ def lib() -> C.CDLL:
     L.mmoe_fp8_workspace.argtypes = [C.POINTER(Config), i64, C.POINTER(C.c_size_t)]
     L.mmoe_forward_fp8.argtypes = [C.POINTER(Config), C.POINTER(FP8Weights), vp, i64, vp, i32, vp, vp, vp, vp, C.c_size_t,
                                    vp]
+    L.mmoe_fp8_status.argtypes = []
+    L.mmoe_debug_fp8_waits.argtypes = [i64, i32]
     L.mmoe_block_norm.argtypes = [vp, vp]  # a Norm by reference, or its bytes
     for name in EXPORTS:
         if name != "mmoe_last_error":

@@ -26,7 +26,16 @@ namespace f8 {
 
 constexpr int kBlk = 128;             // features (and weight rows) per scale
 constexpr float kTop = 448.0f;        // largest finite e4m3 value
-constexpr long long kWaitClk = 4000000000ll;  // about 2 s of SM clock: the limit of every device-side wait
+constexpr long long kWaitClk = 4000000000ll;  // about 2 s of SM clock: how long a device-side wait lasts before it gives up
+constexpr long long kDrainClk = 200000000ll;  // about 0.1 s: then a kernel that gives up no longer waits for its copies or MMAs
+
+// How long the waits of a launch last, and where one that gives up says so.
+struct Waits {
+    int* err;         // host-visible word, set to the wait's site
+    long long limit;  // SM clocks
+    int stall;        // failure-detection tests: 1: the first CTA's MMA warps wait for a barrier that nothing signals; 2: so
+                      // do the promotion warps of the first cluster's last CTA
+};
 
 inline int64_t blocks_of(int64_t n) { return (n + kBlk - 1) / kBlk; }
 
@@ -283,19 +292,24 @@ __device__ __forceinline__ float4 peer_load4(uint32_t addr) {
     return v;
 }
 
-// A bounded mbarrier wait.  Gives up after kWaitClk, or once another thread of the CTA has given up;
-// then it sets the CTA's abort word and the host-visible flag and returns false.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort_word, int* err, int site) {
+// Tells the CTA's other threads, and the host, that a wait has run out.
+__device__ __forceinline__ void give_up(int* abort_word, const Waits& w, int site) {
+    atomicExch(abort_word, 1);
+    *reinterpret_cast<volatile int*>(w.err) = site;
+    __threadfence_system();
+}
+
+// A bounded mbarrier wait.  It ends without the barrier (and returns false) after the launch's limit, which it then reports,
+// or once another thread of the CTA has given up.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort_word, const Waits& w, int site) {
     if (async::mbar_try_wait(bar, parity)) return true;
     const long long t0 = async::clk();
     for (;;) {
         for (int i = 0; i < 64; ++i)
             if (async::mbar_try_wait(bar, parity)) return true;
         if (*reinterpret_cast<volatile int*>(abort_word)) return false;
-        if (async::clk() - t0 > kWaitClk) {
-            atomicExch(abort_word, 1);
-            *reinterpret_cast<volatile int*>(err) = site;
-            __threadfence_system();
+        if (async::clk() - t0 > w.limit) {
+            give_up(abort_word, w, site);
             return false;
         }
     }
@@ -306,7 +320,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort_
 __device__ __forceinline__ void peer_arrive(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int* abort_word, int* err, int site) {
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int* abort_word, const Waits& w, int site) {
     const long long t0 = async::clk();
     for (;;) {
         uint32_t done;
@@ -319,10 +333,8 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int
             : "memory");
         if (done) return true;
         if (*reinterpret_cast<volatile int*>(abort_word)) return false;
-        if (async::clk() - t0 > kWaitClk) {
-            atomicExch(abort_word, 1);
-            *reinterpret_cast<volatile int*>(err) = site;
-            __threadfence_system();
+        if (async::clk() - t0 > w.limit) {
+            give_up(abort_word, w, site);
             return false;
         }
     }
@@ -330,18 +342,14 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int
 
 // The same by a whole warp, which decides as one.  Every lane polls: against one lane that polls and a shuffle that
 // tells the others, a block of 128 of the promotion loops took 639 instead of 1042 clocks.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort_word, int* err, int site) {
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort_word, const Waits& w, int site) {
     if (__all_sync(0xffffffffu, async::mbar_try_wait(bar, parity))) return true;
     const long long t0 = async::clk();
     for (;;) {
         for (int i = 0; i < 64; ++i)
             if (__all_sync(0xffffffffu, async::mbar_try_wait(bar, parity))) return true;
-        const bool late = async::clk() - t0 > kWaitClk;
-        if (late) {
-            atomicExch(abort_word, 1);
-            *reinterpret_cast<volatile int*>(err) = site;
-            __threadfence_system();
-        }
+        const bool late = async::clk() - t0 > w.limit;
+        if (late) give_up(abort_word, w, site);
         if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile int*>(abort_word))) return false;
     }
 }
@@ -354,11 +362,11 @@ __device__ __forceinline__ void peer_arrive_read(uint32_t addr) {
 }
 
 // Both of two barriers.
-__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, int* abort_word, int* err,
-                                           int site) {
+__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, int* abort_word,
+                                           const Waits& w, int site) {
     const bool first = async::mbar_try_wait(a, pa), both = async::mbar_try_wait(b, pb) && first;
     if (__all_sync(0xffffffffu, both)) return true;
-    return warp_wait(a, pa, abort_word, err, site) && warp_wait(b, pb, abort_word, err, site);
+    return warp_wait(a, pa, abort_word, w, site) && warp_wait(b, pb, abort_word, w, site);
 }
 
 // One lane of a converged warp, the same each time.
@@ -372,11 +380,12 @@ __device__ __forceinline__ bool elect() {
     return p != 0;
 }
 
-// The wait used while draining: ignores the abort word.
+// The wait of a kernel that has given up, for its own copies and MMAs in flight: it ignores the abort word and has a limit of
+// its own, long beside any copy.
 __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) {
     const long long t0 = async::clk();
     while (!async::mbar_try_wait(bar, parity))
-        if (async::clk() - t0 > kWaitClk) return;
+        if (async::clk() - t0 > kDrainClk) return;
 }
 
 // Lets a kernel have as much dynamic shared memory as a CTA can (asked for once a device: the call is not free).
@@ -429,7 +438,7 @@ struct Product {
     void* y;
     bool y_bf16;
     int64_t ldy;
-    int* err;
+    Waits waits;
 };
 cudaError_t launch_product(const Product& p, cudaStream_t st);
 cudaError_t launch_product_small(const Product& p, cudaStream_t st);

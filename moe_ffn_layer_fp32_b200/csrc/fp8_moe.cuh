@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "fp8.cuh"
+
 namespace mmoe {
 namespace f8 {
 
@@ -37,7 +39,7 @@ struct MoePlan {
     float* sx;                 // [T, ceil(d/128)]
     uint8_t* xq;               // [T, d]
     float* part;               // [T, k, d] expert outputs, then [parts, T, d] of the shared one
-    int* err;
+    Waits waits;
 };
 
 // Sets the parts of the shared expert, lays the workspace out from `base`, returns its size.

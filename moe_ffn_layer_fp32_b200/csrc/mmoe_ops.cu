@@ -2,6 +2,7 @@
 // quantisers, products and MoE layer, and the block norm.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "fp8.cuh"
@@ -19,29 +20,41 @@ constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 int* g_flag[kMaxDevices] = {};
 
-mmoe_status device_flag(int** flag) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+std::atomic<long long> g_limit{f8::kWaitClk};  // mmoe_debug_fp8_waits
+std::atomic<int> g_stall{0};
+
+mmoe_status current_device(int* dev) {
+    const cudaError_t e = cudaGetDevice(dev);
     if (e != cudaSuccess) return report_cuda(e, "cudaGetDevice");
-    if (dev < 0 || dev >= kMaxDevices) return report(MMOE_ERR_INVALID_ARG, "device %d: unsupported index", dev);
+    if (*dev < 0 || *dev >= kMaxDevices) return report(MMOE_ERR_INVALID_ARG, "device %d: unsupported index", *dev);
+    return MMOE_OK;
+}
+
+// Reports, once, a wait that gave up on the device (g_mu is held).
+mmoe_status take_timeout(int dev) {
+    const int site = g_flag[dev] ? __atomic_exchange_n(g_flag[dev], 0, __ATOMIC_ACQ_REL) : 0;
+    return site ? report(MMOE_ERR_TIMEOUT, "a kernel of an earlier call gave up waiting (site %d)", site) : MMOE_OK;
+}
+
+// What the waits of the next launch on the current device are told.
+mmoe_status device_waits(f8::Waits* w) {
+    int dev = 0;
+    const mmoe_status st = current_device(&dev);
+    if (st != MMOE_OK) return st;
     std::lock_guard<std::mutex> lock(g_mu);
     if (!g_flag[dev]) {
         cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
         int* p = nullptr;
         cudaThreadExchangeStreamCaptureMode(&mode);
-        e = cudaHostAlloc(reinterpret_cast<void**>(&p), sizeof(int), cudaHostAllocMapped | cudaHostAllocPortable);
+        const cudaError_t e = cudaHostAlloc(reinterpret_cast<void**>(&p), sizeof(int), cudaHostAllocMapped | cudaHostAllocPortable);
         cudaThreadExchangeStreamCaptureMode(&mode);
         if (e != cudaSuccess) return report_cuda(e, "flag allocation");
         *p = 0;
         g_flag[dev] = p;  // device and host address are the same under unified addressing
     }
-    volatile int* v = g_flag[dev];
-    if (*v != 0) {
-        const int site = *v;
-        *v = 0;
-        return report(MMOE_ERR_TIMEOUT, "a kernel of an earlier call gave up waiting (site %d)", site);
-    }
-    *flag = g_flag[dev];
+    const mmoe_status late = take_timeout(dev);
+    if (late != MMOE_OK) return late;
+    *w = f8::Waits{g_flag[dev], g_limit.load(), g_stall.exchange(0)};
     return MMOE_OK;
 }
 
@@ -218,8 +231,8 @@ mmoe_status mmoe_gemm_fp8(const uint8_t* a, const float* sa, int64_t M, const ui
     CHECK(check_product(M, w, sw, 1, N, K, y, y_type, ldy));
     CHECK(check_codes(a, sa, M, K, y, ((M - 1) * ldy + N) * size_of(y_type)));
     if (M == 0) return MMOE_OK;
-    f8::Product p = {a, sa, nullptr, 0, w, sw, M, (int)N, (int)K, 0, nullptr, y, y_type == MMOE_BF16, ldy, nullptr};
-    CHECK(device_flag(&p.err));
+    f8::Product p = {a, sa, nullptr, 0, w, sw, M, (int)N, (int)K, 0, nullptr, y, y_type == MMOE_BF16, ldy, {}};
+    CHECK(device_waits(&p.waits));
     const cudaError_t e = M <= f8::kSmallRows ? f8::launch_product_small(p, (cudaStream_t)stream)
                                               : f8::launch_product(p, (cudaStream_t)stream);
     return e == cudaSuccess ? MMOE_OK : report_cuda(e, "product launch");
@@ -238,8 +251,8 @@ mmoe_status mmoe_gemm_fp8_grouped(const uint8_t* a, const float* sa, int64_t M, 
     if (overlap(y, ((M - 1) * ldy + N) * size_of(y_type), offsets, 4 * (groups + 1)))
         return report(MMOE_ERR_INVALID_ARG, "y overlaps the offsets");
     f8::Product p = {a, sa, nullptr, 0, w, sw, M, (int)N, (int)K, (int)groups, offsets, y, y_type == MMOE_BF16, ldy,
-                     nullptr};
-    CHECK(device_flag(&p.err));
+                     {}};
+    CHECK(device_waits(&p.waits));
     const cudaError_t e = f8::launch_product(p, (cudaStream_t)stream);
     return e == cudaSuccess ? MMOE_OK : report_cuda(e, "grouped product launch");
 }
@@ -264,10 +277,10 @@ mmoe_status mmoe_linear_fp8(const uint16_t* x_bf16, int64_t M, int64_t ldx, cons
     const int64_t xb = ((M - 1) * ldx + K) * 2, yb = ((M - 1) * ldy + N) * size_of(y_type);
     if (overlap(x_bf16, xb, y, yb)) return report(MMOE_ERR_INVALID_ARG, "x and y overlap");
     f8::Product p = {nullptr, nullptr, reinterpret_cast<const __nv_bfloat16*>(x_bf16), ldx, w, sw, M, (int)N, (int)K, 0,
-                     nullptr, y, y_type == MMOE_BF16, ldy, nullptr};
+                     nullptr, y, y_type == MMOE_BF16, ldy, {}};
     const cudaStream_t st = (cudaStream_t)stream;
     if (M <= f8::kSmallRows) {
-        CHECK(device_flag(&p.err));
+        CHECK(device_waits(&p.waits));
         const cudaError_t e = f8::launch_product_small(p, st);
         return e == cudaSuccess ? MMOE_OK : report_cuda(e, "linear launch");
     }
@@ -278,7 +291,7 @@ mmoe_status mmoe_linear_fp8(const uint16_t* x_bf16, int64_t M, int64_t ldx, cons
         overlap(workspace, (int64_t)need, w, N * K) ||
         overlap(workspace, (int64_t)need, sw, f8::blocks_of(N) * f8::blocks_of(K) * 4))
         return report(MMOE_ERR_INVALID_ARG, "the workspace overlaps x, y, the weights or their scales");
-    CHECK(device_flag(&p.err));
+    CHECK(device_waits(&p.waits));
     float* s = static_cast<float*>(workspace);
     uint8_t* q = static_cast<uint8_t*>(workspace) + scale_bytes(M, K);
     cudaError_t e = f8::launch_quantize_rows(x_bf16, true, M, K, ldx, q, s, st);
@@ -338,7 +351,7 @@ mmoe_status mmoe_forward_fp8(const mmoe_config* cfg, const mmoe_fp8_weights* w, 
         for (int j = 0; j < i; ++j) bad = bad || overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes);
         if (bad) return report(MMOE_ERR_INVALID_ARG, "an output or the workspace overlaps another buffer");
     }
-    CHECK(device_flag(&p.err));
+    CHECK(device_waits(&p.waits));
     f8::carve_moe(p, static_cast<unsigned char*>(workspace));
     p.w_router = w->w_router;
     p.router_bias = cfg->has_router_bias ? w->router_bias : nullptr;
@@ -358,6 +371,21 @@ mmoe_status mmoe_forward_fp8(const mmoe_config* cfg, const mmoe_fp8_weights* w, 
     p.out_counts = expert_counts;
     const cudaError_t e = f8::launch_moe_few(p, (cudaStream_t)stream);
     return e == cudaSuccess ? MMOE_OK : report_cuda(e, "MoE layer launch");
+}
+
+mmoe_status mmoe_fp8_status(void) {
+    int dev = 0;
+    CHECK(current_device(&dev));
+    std::lock_guard<std::mutex> lock(g_mu);
+    return take_timeout(dev);
+}
+
+mmoe_status mmoe_debug_fp8_waits(int64_t clocks, int32_t stall_next) {
+    if (clocks < 0) return report(MMOE_ERR_INVALID_ARG, "clocks=%lld: must be >= 0", (long long)clocks);
+    if (stall_next < 0 || stall_next > 2) return report(MMOE_ERR_INVALID_ARG, "stall_next=%d: must be 0, 1 or 2", stall_next);
+    g_limit.store(clocks ? clocks : f8::kWaitClk);
+    g_stall.store(stall_next);
+    return MMOE_OK;
 }
 
 mmoe_status mmoe_block_norm(const mmoe_norm* n, void* stream) {

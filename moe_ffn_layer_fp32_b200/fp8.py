@@ -42,6 +42,14 @@ def _output(y, M: int, N: int, out_dtype, x: torch.Tensor):
     return y, TYPE[y.dtype], rows_of(y, N, "y")
 
 
+def check_timeouts(device=None) -> None:
+    """Raises MMoEError (TIMEOUT), once, where a bounded wait of a product or layer call on ``device`` (default: the
+    current one) has given up.  The next such call would raise it too; this is for replays of captured graphs and for
+    the end of a program, and knows of work that has ended: synchronise first."""
+    with torch.cuda.device(device):
+        check(lib().mmoe_fp8_status())
+
+
 def quantize_fp8_rows(x: torch.Tensor, *, stream=None):
     """x [rows, K] (float32 or bfloat16, rows contiguous, K a multiple of 8) -> (codes [rows, K], scales
     [rows, ceil(K / 128)])."""
