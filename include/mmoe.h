@@ -493,12 +493,12 @@ mmoe_status mmoe_fp8_status(void);
 
 /* Failure detection without a GPU fault, as mmoe_debug_set_wait_limit: from now
  * on the bounded waits of the products and the layer, on every device, last
- * `clocks` SM clocks (0: the default, about 4e9).  With stall_next = 1 or 2 the
- * next one of these calls makes one CTA of its kernel wait for a barrier that
- * nothing signals: 1 those of its warps that issue the matrix instructions, 2
- * those that add up what they produce, in the last CTA of the first cluster
- * or pair.  A captured call keeps both values in its graph.  A caller has no reason to call this
- * outside tests.  Errors: INVALID_ARG (clocks < 0, stall_next not 0, 1 or 2). */
+ * `clocks` SM clocks (0: the default, about 4e9).  With stall_next = 1 or 2, in
+ * the next one of these calls the barriers of one CTA expect an arrival that
+ * never comes: 1 those that its warps wait for before they issue matrix
+ * instructions, 2 those before they read the results, in the last CTA of the
+ * first cluster or pair.  A captured call keeps both values in its graph.  A
+ * caller has no reason to call this outside tests.  Errors: INVALID_ARG (clocks < 0, stall_next not 0, 1 or 2). */
 mmoe_status mmoe_debug_fp8_waits(int64_t clocks, int32_t stall_next);
 
 /* ---- between two blocks -----------------------------------------------------

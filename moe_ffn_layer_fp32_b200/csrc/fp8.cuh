@@ -33,8 +33,10 @@ constexpr long long kDrainClk = 200000000ll;  // about 0.1 s: then a kernel that
 struct Waits {
     int* err;         // host-visible word, set to the wait's site
     long long limit;  // SM clocks
-    int stall;        // failure-detection tests: 1: the first CTA's MMA warps wait for a barrier that nothing signals; 2: so
-                      // do the promotion warps of the first cluster's last CTA
+    int stall;        // failure-detection tests: 1: in the first CTA the MMA warps' barriers expect an arrival more than there
+                      // is, 2: in the first cluster's last CTA those of the promotion warps
+    // What CTA `cta` adds to the arrivals that the barriers of 1: the MMA, 2: the promotion warps expect.
+    __device__ __forceinline__ int missing(int who, unsigned cta) const { return stall == who && blockIdx.x == cta; }
 };
 
 inline int64_t blocks_of(int64_t n) { return (n + kBlk - 1) / kBlk; }
@@ -292,24 +294,38 @@ __device__ __forceinline__ float4 peer_load4(uint32_t addr) {
     return v;
 }
 
-// Tells the CTA's other threads, and the host, that a wait has run out.
-__device__ __forceinline__ void give_up(int* abort_word, const Waits& w, int site) {
-    atomicExch(abort_word, 1);
-    *reinterpret_cast<volatile int*>(w.err) = site;
-    __threadfence_system();
-}
+// A CTA's waits, in its shared memory (as kernel arguments in each wait they took registers: the product of 512 x 2048 x
+// 2048 11.6 us instead of 10.7).
+struct Stop {
+    long long limit;
+    int set;  // a wait has run out
+    __device__ __forceinline__ void init(const Waits& w) {
+        limit = w.limit;
+        set = 0;
+    }
+    __device__ __forceinline__ bool is_set() const { return *reinterpret_cast<const volatile int*>(&set); }
+    __device__ __forceinline__ bool late(long long t0) const {
+        return async::clk() - t0 > *reinterpret_cast<const volatile long long*>(&limit);
+    }
+    // Tells the CTA's other threads, and the host.
+    __device__ __forceinline__ void give_up(int* err, int site) {
+        atomicExch(&set, 1);
+        *reinterpret_cast<volatile int*>(err) = site;
+        __threadfence_system();
+    }
+};
 
 // A bounded mbarrier wait.  It ends without the barrier (and returns false) after the launch's limit, which it then reports,
 // or once another thread of the CTA has given up.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort_word, const Waits& w, int site) {
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Stop* stop, int* err, int site) {
     if (async::mbar_try_wait(bar, parity)) return true;
     const long long t0 = async::clk();
     for (;;) {
         for (int i = 0; i < 64; ++i)
             if (async::mbar_try_wait(bar, parity)) return true;
-        if (*reinterpret_cast<volatile int*>(abort_word)) return false;
-        if (async::clk() - t0 > w.limit) {
-            give_up(abort_word, w, site);
+        if (stop->is_set()) return false;
+        if (stop->late(t0)) {
+            stop->give_up(err, site);
             return false;
         }
     }
@@ -320,7 +336,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort_
 __device__ __forceinline__ void peer_arrive(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int* abort_word, const Waits& w, int site) {
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, Stop* stop, int* err, int site) {
     const long long t0 = async::clk();
     for (;;) {
         uint32_t done;
@@ -332,9 +348,9 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int
             : "r"(async::su32(bar)), "r"(parity)
             : "memory");
         if (done) return true;
-        if (*reinterpret_cast<volatile int*>(abort_word)) return false;
-        if (async::clk() - t0 > w.limit) {
-            give_up(abort_word, w, site);
+        if (stop->is_set()) return false;
+        if (stop->late(t0)) {
+            stop->give_up(err, site);
             return false;
         }
     }
@@ -342,15 +358,15 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int
 
 // The same by a whole warp, which decides as one.  Every lane polls: against one lane that polls and a shuffle that
 // tells the others, a block of 128 of the promotion loops took 639 instead of 1042 clocks.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort_word, const Waits& w, int site) {
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Stop* stop, int* err, int site) {
     if (__all_sync(0xffffffffu, async::mbar_try_wait(bar, parity))) return true;
     const long long t0 = async::clk();
     for (;;) {
         for (int i = 0; i < 64; ++i)
             if (__all_sync(0xffffffffu, async::mbar_try_wait(bar, parity))) return true;
-        const bool late = async::clk() - t0 > w.limit;
-        if (late) give_up(abort_word, w, site);
-        if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile int*>(abort_word))) return false;
+        const bool late = stop->late(t0);
+        if (late) stop->give_up(err, site);
+        if (__any_sync(0xffffffffu, late || stop->is_set())) return false;
     }
 }
 
@@ -362,11 +378,11 @@ __device__ __forceinline__ void peer_arrive_read(uint32_t addr) {
 }
 
 // Both of two barriers.
-__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, int* abort_word,
-                                           const Waits& w, int site) {
+__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, Stop* stop,
+                                           int* err, int site) {
     const bool first = async::mbar_try_wait(a, pa), both = async::mbar_try_wait(b, pb) && first;
     if (__all_sync(0xffffffffu, both)) return true;
-    return warp_wait(a, pa, abort_word, w, site) && warp_wait(b, pb, abort_word, w, site);
+    return warp_wait(a, pa, stop, err, site) && warp_wait(b, pb, stop, err, site);
 }
 
 // One lane of a converged warp, the same each time.
@@ -380,7 +396,7 @@ __device__ __forceinline__ bool elect() {
     return p != 0;
 }
 
-// The wait of a kernel that has given up, for its own copies and MMAs in flight: it ignores the abort word and has a limit of
+// The wait of a kernel that has given up, for its own copies and MMAs in flight: it does not look at the stop and has a limit of
 // its own, long beside any copy.
 __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) {
     const long long t0 = async::clk();

@@ -127,10 +127,9 @@ struct Smem {
     uint64_t full[kStages], empty[kStages];
     uint64_t accf[kMaxBufs], acce[kMaxBufs];
     uint64_t tfull[kTInfo], tempty[kTInfo];
-    uint64_t never;                                                // signalled by nothing: the stall of the failure tests
     TileInfo ti[kTInfo];
     uint32_t tmem;
-    int abort;
+    Stop stop;
 };
 
 // Walks over the groups of a grouped product in a warp's registers, 32 groups at a time (a lane a group).  The offsets are
@@ -240,15 +239,14 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
             mbar_init(&sm->empty[i], 1);
         }
         for (int i = 0; i < kBufs; ++i) {
-            mbar_init(&sm->accf[i], 1);
-            mbar_init(&sm->acce[i], C * kPromoWarps);
+            mbar_init(&sm->accf[i], 1 + p.waits.missing(2, C - 1));
+            mbar_init(&sm->acce[i], C * kPromoWarps + p.waits.missing(1, 0));
         }
         for (int i = 0; i < kTInfo; ++i) {
             mbar_init(&sm->tfull[i], 1);
             mbar_init(&sm->tempty[i], kIssuers + kPromoWarps);
         }
-        mbar_init(&sm->never, 1);
-        sm->abort = 0;
+        sm->stop.init(p.waits);
         async::fence_barrier_init();
     }
     if (warp == 1) {
@@ -275,10 +273,7 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
             bool ok = true;
             for (int64_t L = blockIdx.x / C; ok; L += gridDim.x / C, ++tc) {
                 const int b = tc % kTInfo;
-                if (tc >= kTInfo && !warp_wait(&sm->tempty[b], (tc / kTInfo - 1) & 1, &sm->abort, p.waits, 1)) {
-                    ok = false;
-                    break;
-                }
+                if (tc >= kTInfo && !warp_wait(&sm->tempty[b], (tc / kTInfo - 1) & 1, &sm->stop, p.waits.err, 1)) break;
                 TileInfo& ti = sm->ti[b];
                 // column tiles innermost: the CTAs that run together share activation tiles in L2
                 const int64_t mt = L / ntiles;
@@ -309,7 +304,7 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                 const uint32_t tx = kPair ? (second ? 4 : 3) * kTileBytes : kTileBytes + Sm::kWeights;
                 for (int kb = 0; kb < KB; ++kb, ++sc) {
                     const int s = sc % S;
-                    if (sc >= S && !warp_wait(&sm->empty[s], (sc / S - 1) & 1, &sm->abort, p.waits, 2)) {
+                    if (sc >= S && !warp_wait(&sm->empty[s], (sc / S - 1) & 1, &sm->stop, p.waits.err, 2)) {
                         ok = false;
                         break;
                     }
@@ -330,13 +325,11 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                     __syncwarp();
                 }
             }
-            // Every copy has landed and every stage has been released before the CTA may exit.  After a wait that gave up,
-            // the copies in flight: CTA 0's barriers count those of both, where CTA 1 may have sent other blocks (then
-            // they wait their limit), and CTA 1, which has no barrier for its own, gives them about 1 ms.
-            for (int i = max(sc - S, 0); i < sc && ok; ++i) ok = warp_wait(&sm->empty[i % S], (i / S) & 1, &sm->abort, p.waits, 5);
-            if (!ok && rank == 0) {
+            // Every copy has landed before the CTA may exit.  CTA 0's barriers count those of both; after a wait that gave up
+            // CTA 1 may have sent others, which no barrier tells of: they are given about 1 ms.
+            if (rank == 0) {
                 for (int i = max(sc - S, 0); i < sc; ++i) wait_drain(&sm->full[i % S], (i / S) & 1);
-            } else if (!ok) {
+            } else if (sm->stop.is_set()) {
                 const long long t0 = async::clk();
                 while (async::clk() - t0 < kLandClk) {
                 }
@@ -350,10 +343,10 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
             static_assert(S % kIssuers == 0 && kBufs % kIssuers == 0, "ownership");
             const uint64_t ring_desc = tc5::smem_desc_sw128(sm->ring[0]);
             int sc = 0, mine = warp - 1, tc = 0, last = -1;  // blocks of K so far, this warp's next; its last buffer
-            bool ok = p.waits.stall != 1 || blockIdx.x != 0 || warp_wait(&sm->never, 0, &sm->abort, p.waits, 9);
+            bool ok = true;
             while (ok) {
                 const int b = tc % kTInfo;
-                if (!warp_wait(&sm->tfull[b], (tc / kTInfo) & 1, &sm->abort, p.waits, 3)) break;
+                if (!warp_wait(&sm->tfull[b], (tc / kTInfo) & 1, &sm->stop, p.waits.err, 3)) break;
                 const int end = sm->ti[b].end;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm->tempty[b]);
@@ -363,7 +356,7 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                 sc += KB;
                 for (; mine < sc && ok; mine += kIssuers) {
                     const int s = mine % S, d = mine % kBufs;
-                    ok = warp_wait2(&sm->full[s], (mine / S) & 1, &sm->acce[d], (mine / kBufs) & 1, &sm->abort, p.waits, 4);
+                    ok = warp_wait2(&sm->full[s], (mine / S) & 1, &sm->acce[d], (mine / kBufs) & 1, &sm->stop, p.waits.err, 4);
                     if (!ok) break;
                     tc5::after_sync();
                     const uint64_t ad = ring_desc + (uint64_t)(s * ((kTileBytes + Sm::kWeights) >> 4)), wd = ad + (kTileBytes >> 4);
@@ -386,8 +379,11 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                     last = mine;
                 }
             }
-            // every MMA has completed before TMEM is released
-            if (last >= 0) wait_drain(&sm->accf[last % kBufs], (last / kBufs) & 1);
+            // every MMA has completed before TMEM is released, and the last commits have arrived before the CTA may exit
+            if (last >= 0) {
+                wait_drain(&sm->accf[last % kBufs], (last / kBufs) & 1);
+                wait_drain(&sm->empty[last % S], (last / S) & 1);
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
@@ -410,7 +406,7 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
         };
         const auto next = [&]() -> bool {
             const int tb = tc % kTInfo;
-            if (!warp_wait(&sm->tfull[tb], (tc / kTInfo) & 1, &sm->abort, p.waits, 6)) return false;
+            if (!warp_wait(&sm->tfull[tb], (tc / kTInfo) & 1, &sm->stop, p.waits.err, 6)) return false;
             ti = sm->ti[tb];
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->tempty[tb]);
@@ -423,13 +419,13 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
             scales(1, KB > 1 ? 1 : 0);
             return true;
         };
-        bool more = (p.waits.stall != 2 || blockIdx.x != C - 1 || warp_wait(&sm->never, 0, &sm->abort, p.waits, 9)) && next();
+        bool more = next();
         while (more) {
             float2 acc[kCols / 2];
 #pragma unroll
             for (int c = 0; c < kCols / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
             uint32_t v[2][32];
-            bool ok = warp_wait(&sm->accf[n % kBufs], (n / kBufs) & 1, &sm->abort, p.waits, 7);
+            bool ok = warp_wait(&sm->accf[n % kBufs], (n / kBufs) & 1, &sm->stop, p.waits.err, 7);
             if (ok) {
                 tc5::after_sync();
                 tc5::tmem_ld32(tl + n % kBufs * kBuf, v[0]);
@@ -462,14 +458,14 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                     }
                 }
                 if (kb + 1 < KB) {
-                    ok = warp_wait(after, (n / kBufs) & 1, &sm->abort, p.waits, 8);
+                    ok = warp_wait(after, (n / kBufs) & 1, &sm->stop, p.waits.err, 8);
                     if (ok) {
                         tc5::after_sync();
                         tc5::tmem_ld32(tl + n % kBufs * kBuf, v[0]);
                     }
                 }
             }
-            if (!ok || __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&sm->abort))) break;
+            if (!ok || __any_sync(0xffffffffu, sm->stop.is_set())) break;
             constexpr int kBox = 128 / (int)sizeof(T);           // columns of a box
             constexpr int kRound = Sm::kOut / (32 * 128);        // boxes staged at once
             const int64_t y0 = ti.row0 + quarter * 32;
@@ -536,9 +532,9 @@ struct SmallSmem {
     alignas(1024) uint8_t ring[kRing][kTileBytes];
     alignas(1024) uint8_t b[kOperand];       // [block][NT rows][128 bytes], swizzled; then the partial sums [NT][128]
     float sx[kOperand / (NT * kBlk)][NT];
-    uint64_t full[kRing], empty[kRing], accf[kSBufs], acce[kSBufs], ready, drained, never;
+    uint64_t full[kRing], empty[kRing], accf[kSBufs], acce[kSBufs], ready, drained;
     uint32_t tmem;
-    int abort;
+    Stop stop;
 };
 
 // Codes and scales of the activation rows of n blocks of K, those of this CTA from its i0-th on, into the operand buffer: 8
@@ -620,13 +616,12 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
             mbar_init(&sm->empty[i], 1);
         }
         for (int i = 0; i < kSBufs; ++i) {
-            mbar_init(&sm->accf[i], 1);
-            mbar_init(&sm->acce[i], 4);
+            mbar_init(&sm->accf[i], 1 + p.waits.missing(2, C - 1));
+            mbar_init(&sm->acce[i], 4 + p.waits.missing(1, 0));
         }
         mbar_init(&sm->ready, 32 * quant_warps<NT>());
         mbar_init(&sm->drained, 4);
-        mbar_init(&sm->never, 1);
-        sm->abort = 0;
+        sm->stop.init(p.waits);
         async::fence_barrier_init();
     }
     if (warp == 1) {
@@ -645,23 +640,19 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
             int i = 0;
             for (; i < mine; ++i) {
                 const int s = i % kRing;
-                if (i >= kRing && !wait(&sm->empty[s], (i / kRing - 1) & 1, &sm->abort, p.waits, 11)) break;
+                if (i >= kRing && !wait(&sm->empty[s], (i / kRing - 1) & 1, &sm->stop, p.waits.err, 11)) break;
                 mbar_expect_tx(&sm->full[s], kTileBytes);
                 tc5::tma_load_2d(sm->ring[s], &wmap, (rank + i * C) * kBlk, nt * kBlk, &sm->full[s]);
             }
-            // every copy has landed and every slot has been released before the CTA may exit
-            bool ok = i == mine;
-            for (int j = max(i - kRing, 0); j < i && ok; ++j) ok = wait(&sm->empty[j % kRing], (j / kRing) & 1, &sm->abort, p.waits, 19);
-            for (int j = max(i - kRing, 0); j < i && !ok; ++j) wait_drain(&sm->full[j % kRing], (j / kRing) & 1);
+            for (int j = max(i - kRing, 0); j < i; ++j) wait_drain(&sm->full[j % kRing], (j / kRing) & 1);
         }
     } else if (warp == 1) {
         int i = 0;
-        const bool go = p.waits.stall != 1 || blockIdx.x != 0 || warp_wait(&sm->never, 0, &sm->abort, p.waits, 20);
-        for (; i < mine && go; ++i) {
+        for (; i < mine; ++i) {
             const int s = i % kRing, d = i % kSBufs, r = i % kRound;
-            if (r == 0 && !warp_wait(&sm->ready, (i / kRound) & 1, &sm->abort, p.waits, 12)) break;
-            if (!warp_wait(&sm->full[s], (i / kRing) & 1, &sm->abort, p.waits, 13) ||
-                !warp_wait(&sm->acce[d], (i / kSBufs) & 1, &sm->abort, p.waits, 14))
+            if (r == 0 && !warp_wait(&sm->ready, (i / kRound) & 1, &sm->stop, p.waits.err, 12)) break;
+            if (!warp_wait(&sm->full[s], (i / kRing) & 1, &sm->stop, p.waits.err, 13) ||
+                !warp_wait(&sm->acce[d], (i / kSBufs) & 1, &sm->stop, p.waits.err, 14))
                 break;
             tc5::after_sync();
             const uint64_t wd = tc5::smem_desc_sw128(sm->ring[s]);
@@ -675,10 +666,13 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
             }
             __syncwarp();
         }
-        if (i > 0) wait_drain(&sm->accf[(i - 1) % kSBufs], ((i - 1) / kSBufs) & 1);
+        if (i > 0) {  // the last commits have arrived
+            wait_drain(&sm->accf[(i - 1) % kSBufs], ((i - 1) / kSBufs) & 1);
+            wait_drain(&sm->empty[(i - 1) % kRing], ((i - 1) / kRing) & 1);
+        }
     } else if (warp >= 6) {
         for (int i0 = 0; i0 < mine; i0 += kRound) {
-            if (i0 > 0 && !warp_wait(&sm->drained, (i0 / kRound - 1) & 1, &sm->abort, p.waits, 18)) break;
+            if (i0 > 0 && !warp_wait(&sm->drained, (i0 / kRound - 1) & 1, &sm->stop, p.waits.err, 18)) break;
             encode_rows<NT>(p, sm, rank, C, KB, i0, min(kRound, mine - i0), tid - 64);
         }
     } else {
@@ -691,22 +685,21 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
 #pragma unroll
         for (int c = 0; c < NT / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
         const float* sw = p.sw + (int64_t)nt * KB + rank;
-        const bool go = p.waits.stall != 2 || blockIdx.x != C - 1 || warp_wait(&sm->never, 0, &sm->abort, p.waits, 20);
-        for (int i0 = 0; i0 < mine && go; i0 += kRound) {
+        for (int i0 = 0; i0 < mine; i0 += kRound) {
             if (i0 > 0) {  // the operand buffer and its scales are free once every warp has added the last round
                 if (lane == 0) mbar_arrive(&sm->drained);
-                if (!warp_wait(&sm->drained, (i0 / kRound - 1) & 1, &sm->abort, p.waits, 17)) break;
+                if (!warp_wait(&sm->drained, (i0 / kRound - 1) & 1, &sm->stop, p.waits.err, 17)) break;
             }
             const int n = min(kRound, mine - i0);
             encode_rows<NT>(p, sm, rank, C, KB, i0, n, pt);
-            if (!warp_wait(&sm->ready, (i0 / kRound) & 1, &sm->abort, p.waits, 15)) break;
+            if (!warp_wait(&sm->ready, (i0 / kRound) & 1, &sm->stop, p.waits.err, 15)) break;
             float ws = sw[(int64_t)i0 * C];
             bool ok = true;
             for (int r = 0; r < n; ++r) {
                 const int i = i0 + r, d = i % kSBufs;
                 const float w = ws;
                 if (r + 1 < n) ws = sw[(int64_t)(i + 1) * C];
-                if (!warp_wait(&sm->accf[d], (i / kSBufs) & 1, &sm->abort, p.waits, 16)) {
+                if (!warp_wait(&sm->accf[d], (i / kSBufs) & 1, &sm->stop, p.waits.err, 16)) {
                     ok = false;
                     break;
                 }
@@ -741,7 +734,7 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
             }
         } else {
             T* y = static_cast<T*>(p.y) + nt * kBlk + row;
-            if (nt * kBlk + row < p.N && !sm->abort) {
+            if (nt * kBlk + row < p.N && !sm->stop.is_set()) {
 #pragma unroll
                 for (int c = 0; c < NT / 2; ++c) {
                     if (2 * c < m) y[(2 * c) * p.ldy] = (T)acc[c].x;
@@ -754,7 +747,7 @@ product_small_kernel(const __grid_constant__ CUtensorMap wmap, const Product p, 
         __syncwarp();
         cluster_arrive();
         cluster_wait();
-        if (warp >= 2 && !sm->abort) {
+        if (warp >= 2 && !sm->stop.is_set()) {
             // every C-th row is this CTA's: a warp a row, two rows and all the peers' sums in flight
             const int c4 = lane * 4, col = nt * kBlk + c4;
             for (int i0 = warp - 2; rank + C * i0 < m; i0 += 2 * quant_warps<NT>()) {

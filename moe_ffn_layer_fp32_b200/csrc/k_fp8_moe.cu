@@ -191,9 +191,8 @@ struct Layout {
 
 struct ExpertShared {
     uint64_t full[kMaxRing], empty[kMaxRing], accf[kBufs], acce[kBufs], xready, hready, stored, counted, peers, codes;  // from xready on: one phase each
-    uint64_t never;          // signalled by nothing: the stall of the failure tests
     uint32_t tmem;
-    int abort;
+    Stop stop;
     int count[kMaxExperts];
     uint8_t slot[kFewTokens * kMaxTopK];  // the expert of each (token, choice)
     int expert, first, n;    // the cluster's expert (E + i: part i of the shared one; -1: none), its first token in the expert's list, tokens
@@ -241,12 +240,12 @@ __device__ __forceinline__ float2 first_two(const float* w, int KB) { return mak
 // acc = the sum of KB blocks of the tile whose first step is i: w[kb] s[kb][column] times the step's buffer, w01 being
 // first_two(w, KB), read ahead.  The next buffer's load runs under this one's additions.
 __device__ __forceinline__ bool add_blocks(float2 (&acc)[kN / 2], ExpertShared* sm, uint32_t tl, int i, int KB, const float* w,
-                                           float2 w01, const float* s, const Waits& waits, int site) {
+                                           float2 w01, const float* s, int* err, int site) {
 #pragma unroll
     for (int c = 0; c < kN / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
     float w0 = w01.x, w1 = w01.y;
     uint32_t v[2][kN];
-    if (!warp_wait(&sm->accf[i % kBufs], (i / kBufs) & 1, &sm->abort, waits, site)) return false;
+    if (!warp_wait(&sm->accf[i % kBufs], (i / kBufs) & 1, &sm->stop, err, site)) return false;
     tc5::after_sync();
     tmem_ld8(tl + i % kBufs * kCols, v[0]);
     for (int kb0 = 0; kb0 < KB; kb0 += 2) {
@@ -263,7 +262,7 @@ __device__ __forceinline__ bool add_blocks(float2 (&acc)[kN / 2], ExpertShared* 
             if (kb + 2 < KB) w1 = w[kb + 2];
             if (kb + 1 < KB) {
                 const int n = i + kb + 1;
-                if (!warp_wait(&sm->accf[n % kBufs], (n / kBufs) & 1, &sm->abort, waits, site)) return false;
+                if (!warp_wait(&sm->accf[n % kBufs], (n / kBufs) & 1, &sm->stop, err, site)) return false;
                 tc5::after_sync();
                 tmem_ld8(tl + n % kBufs * kCols, v[u ^ 1]);
             }
@@ -399,8 +398,8 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
             mbar_init(&sm->empty[i], 1);
         }
         for (int i = 0; i < kBufs; ++i) {
-            mbar_init(&sm->accf[i], 1);
-            mbar_init(&sm->acce[i], 4);
+            mbar_init(&sm->accf[i], 1 + p.waits.missing(2, S - 1));
+            mbar_init(&sm->acce[i], 4 + p.waits.missing(1, 0));
         }
         mbar_init(&sm->xready, 128);
         mbar_init(&sm->hready, 128);
@@ -408,8 +407,7 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
         mbar_init(&sm->counted, 4);
         mbar_init(&sm->peers, S * 4);
         mbar_init(&sm->codes, S * 4);
-        mbar_init(&sm->never, 1);
-        sm->abort = 0;
+        sm->stop.init(p.waits);
         async::fence_barrier_init();
     }
     if (tid < kMaxExperts) sm->count[tid] = 0;
@@ -456,7 +454,7 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
         int i = 0;
         for (int t = 0, kb = 0; i < steps; ++i) {
             const int s = i % lay.ring;
-            if (i >= lay.ring && !warp_wait(&sm->empty[s], (i / lay.ring - 1) & 1, &sm->abort, p.waits, 21)) break;
+            if (i >= lay.ring && !warp_wait(&sm->empty[s], (i / lay.ring - 1) & 1, &sm->stop, p.waits.err, 21)) break;
             const bool down = i >= ngu;
             if (i == ngu) t = kb = 0;
             if (elect()) {
@@ -475,18 +473,14 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
                 ++t;
             }
         }
-        // every copy has landed and every slot has been released before the CTA may exit
-        bool ok = i == steps;
-        for (int j = max(i - lay.ring, 0); j < i && ok; ++j) ok = warp_wait(&sm->empty[j % lay.ring], (j / lay.ring) & 1, &sm->abort, p.waits, 25);
-        for (int j = max(i - lay.ring, 0); j < i && !ok; ++j) wait_drain(&sm->full[j % lay.ring], (j / lay.ring) & 1);
+        for (int j = max(i - lay.ring, 0); j < i; ++j) wait_drain(&sm->full[j % lay.ring], (j / lay.ring) & 1);
     } else if (warp == 1 || warp == 6) {
         int last = -1;
-        const bool go = p.waits.stall != 1 || blockIdx.x != 0 || warp_wait(&sm->never, 0, &sm->abort, p.waits, 34);
-        for (int i = warp == 1 ? 0 : lay.issuers == 2 ? 1 : steps; i < steps && go; i += lay.issuers) {
+        for (int i = warp == 1 ? 0 : lay.issuers == 2 ? 1 : steps; i < steps; i += lay.issuers) {
             const int s = i % lay.ring, b = i % kBufs;
-            if ((i < 2 && gt > 0 && !warp_wait(&sm->xready, 0, &sm->abort, p.waits, 22)) ||
-                ((i == ngu || i == ngu + 1) && !warp_wait(&sm->hready, 0, &sm->abort, p.waits, 23)) ||
-                !warp_wait2(&sm->full[s], (i / lay.ring) & 1, &sm->acce[b], (i / kBufs) & 1, &sm->abort, p.waits, 24))
+            if ((i < 2 && gt > 0 && !warp_wait(&sm->xready, 0, &sm->stop, p.waits.err, 22)) ||
+                ((i == ngu || i == ngu + 1) && !warp_wait(&sm->hready, 0, &sm->stop, p.waits.err, 23)) ||
+                !warp_wait2(&sm->full[s], (i / lay.ring) & 1, &sm->acce[b], (i / kBufs) & 1, &sm->stop, p.waits.err, 24))
                 break;
             tc5::after_sync();
             const int kb = i < ngu ? i % KBd : (i - ngu) % KBh;
@@ -502,7 +496,10 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
             __syncwarp();
             last = i;
         }
-        if (last >= 0) wait_drain(&sm->accf[last % kBufs], (last / kBufs) & 1);
+        if (last >= 0) {  // the last commits have arrived
+            wait_drain(&sm->accf[last % kBufs], (last / kBufs) & 1);
+            wait_drain(&sm->empty[last % lay.ring], (last / lay.ring) & 1);
+        }
     } else {
         const int pt = tid - 64, quarter = warp & 3, hl = pt & 15;
         const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -544,8 +541,7 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
         }
         fence_async_smem();
         mbar_arrive(&sm->xready);
-        bool ok = warp_wait(&sm->xready, 0, &sm->abort, p.waits, 26);
-        if (p.waits.stall == 2 && blockIdx.x == S - 1) ok = warp_wait(&sm->never, 0, &sm->abort, p.waits, 34) && ok;
+        bool ok = warp_wait(&sm->xready, 0, &sm->stop, p.waits.err, 26);
         int i = 0;
         // gate and up: a lane holds one weight row; lanes l and l + 16 the gate and up rows of a feature
         for (int t = 0; t < gt && ok; ++t) {
@@ -554,7 +550,7 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
             float2 acc[kN / 2];
             const float2 w01 = gate_up_w;
             if (t + 1 < gt) gate_up_w = first_two(gate_up_scales(t + 1), KBd);
-            ok = add_blocks(acc, sm, tl, i, KBd, gate_up_scales(t), w01, sx, p.waits, 27);
+            ok = add_blocks(acc, sm, tl, i, KBd, gate_up_scales(t), w01, sx, p.waits.err, 27);
             i += KBd;
             if (!ok) break;
             // lanes below 16 finish the even tokens, the others the odd ones
@@ -571,9 +567,9 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
         __syncwarp();
         if (lane < S) peer_arrive(peer_addr(&sm->peers, (uint32_t)lane));
         if (ok) {
-            if (lane == 0) ok = wait_cluster(&sm->peers, 0, &sm->abort, p.waits, 32);
+            if (lane == 0) ok = wait_cluster(&sm->peers, 0, &sm->stop, p.waits.err, 32);
             ok = __shfl_sync(0xffffffffu, ok, 0);
-            wait_cluster(&sm->peers, 0, &sm->abort, p.waits, 32);  // each lane's own acquire
+            wait_cluster(&sm->peers, 0, &sm->stop, p.waits.err, 32);  // each lane's own acquire
         }
         if (ok) {
             // A half warp per (token, block).  With few of them each CTA quantises all for itself; with more, 1 / S of
@@ -611,21 +607,21 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
             if (stride != 1) {
                 __syncwarp();
                 if (lane < S) peer_arrive(peer_addr(&sm->codes, (uint32_t)lane));
-                if (lane == 0) ok = wait_cluster(&sm->codes, 0, &sm->abort, p.waits, 33);
+                if (lane == 0) ok = wait_cluster(&sm->codes, 0, &sm->stop, p.waits.err, 33);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
-                wait_cluster(&sm->codes, 0, &sm->abort, p.waits, 33);  // each lane's own acquire
+                wait_cluster(&sm->codes, 0, &sm->stop, p.waits.err, 33);  // each lane's own acquire
             }
         }
         fence_async_smem();
         mbar_arrive(&sm->hready);
-        ok = warp_wait(&sm->hready, 0, &sm->abort, p.waits, 28) && ok;
+        ok = warp_wait(&sm->hready, 0, &sm->stop, p.waits.err, 28) && ok;
         for (int t = 0; t < dt && ok; ++t) {
             const int og = o0 + no * t + quarter;
             const bool mine = quarter < no && og < o1;
             float2 acc[kN / 2];
             const float2 w01 = down_w;
             if (t + 1 < dt) down_w = first_two(down_scales(t + 1), KBh);
-            ok = add_blocks(acc, sm, tl, i, KBh, down_scales(t), w01, sh, p.waits, 29);
+            ok = add_blocks(acc, sm, tl, i, KBh, down_scales(t), w01, sh, p.waits.err, 29);
             i += KBh;
             if (!ok || !mine) continue;
             const int col = og * 32 + lane;
@@ -639,7 +635,7 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
         __threadfence();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->stored);
-        ok = warp_wait(&sm->stored, 0, &sm->abort, p.waits, 30) && ok;
+        ok = warp_wait(&sm->stored, 0, &sm->stop, p.waits.err, 30) && ok;
         if (ok && o1 > o0) {
             if (pt < n) sm->last[pt] = atomicAdd(&p.arrived[sm->token[pt] * kRanks + rank], 1u) == (uint32_t)(p.k + p.parts - 1);
             __syncwarp();
@@ -649,7 +645,7 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
     // every warp helps with these sums
     if (o1 > o0) {
         __syncwarp();
-        if (warp_wait(&sm->counted, 0, &sm->abort, p.waits, 31)) {
+        if (warp_wait(&sm->counted, 0, &sm->stop, p.waits.err, 31)) {
             __threadfence();
             const int quads = (o1 - o0) * 8;  // four columns a thread
             const bool wide = (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;

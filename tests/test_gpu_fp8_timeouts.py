@@ -1,5 +1,5 @@
-"""Bounded waits of the e4m3 products and the layer that run out, without a GPU fault: a barrier that nothing signals, under
-a limit of microseconds.  The kernel drains what it has in flight and returns, the context stays usable, the timeout is
+"""Bounded waits of the e4m3 products and the layer that run out, without a GPU fault: barriers that expect an arrival more
+than there is, under a limit of microseconds.  The kernel drains what it has in flight and returns, the context stays usable, the timeout is
 reported once, and the next call is right again."""
 import pytest
 import torch
