@@ -84,7 +84,8 @@ static __device__ __noinline__ uint32_t divided4(float a, float b, float c, floa
 // (16 either way) every V was checked on the CPU: always the IEEE quotient.  A code that is not 0 needs v >= s 2^-11, and
 // the remainder is a multiple of v 2^-47, which must not underflow; blocks outside that range, of zeros, with NaN or
 // infinities are divided.  (Bounding the quotient from both sides by two products costs less, but BF16 values lie on a
-// border too often: one in 200.)  Quantising 32768 x 2048 BF16 values took 106 us with a division each, and takes 39 us.
+// border too often: one in 200.)  All of it is done for -v / s, whose codes have the other sign: there the
+// correction adds zeros of one sign, while for v / s it made +0 of the code of -0.  Quantising 32768 x 2048 BF16 values took 106 us with a division each, and takes 39 us.
 struct Coder {
     float s, y;
     bool fast;
@@ -93,15 +94,17 @@ struct Coder {
     __device__ __forceinline__ Coder(float scale, float inv) : s(scale), y(inv) {
         fast = scale >= 0x1p-80f && scale <= 0x1p100f;
     }
+    // the codes of -a and -b
     __device__ __forceinline__ uint32_t pair(float a, float b) const {
-        const float2 v = make_float2(a, b), yy = make_float2(y, y), ms = make_float2(-s, -s);
+        const float2 v = make_float2(a, b), yy = make_float2(-y, -y), ss = make_float2(s, s);
         float2 q = __fmul2_rn(v, yy);
-        q = __ffma2_rn(__ffma2_rn(ms, q, v), yy, q);
+        q = __ffma2_rn(__ffma2_rn(ss, q, v), yy, q);
         return e4m3x2(q.x, q.y);
     }
     __device__ __forceinline__ uint2 operator()(const float (&v)[8]) const {
         if (!fast) return make_uint2(divided4(v[0], v[1], v[2], v[3], s), divided4(v[4], v[5], v[6], v[7], s));
-        return make_uint2(pair(v[0], v[1]) | pair(v[2], v[3]) << 16, pair(v[4], v[5]) | pair(v[6], v[7]) << 16);
+        const uint32_t lo = pair(v[0], v[1]) | pair(v[2], v[3]) << 16, hi = pair(v[4], v[5]) | pair(v[6], v[7]) << 16;
+        return make_uint2(lo ^ 0x80808080u, hi ^ 0x80808080u);
     }
 };
 
