@@ -53,7 +53,7 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 
 // max|v| / 448, the IEEE quotient.  Division by a constant after Brisebarre, Muller and Raina ("Accelerating correctly
 // rounded floating-point division when the divisor is known in advance"): the product with the rounded reciprocal and
-// one correction by its remainder.  Checked over every significand; below 2^-100, for infinities and NaN it divides.
+// one correction by its remainder.  Checked over every significand (tests/test_fp8_quotients.py); below 2^-100, for infinities and NaN it divides.
 __device__ __forceinline__ float scale_of(uint32_t amax_bits) {
     const float a = __uint_as_float(amax_bits), q = a * (1.0f / kTop);
     const float s = fmaf(fmaf(-kTop, q, a), 1.0f / kTop, q);
@@ -76,16 +76,18 @@ static __device__ __noinline__ uint32_t divided4(float a, float b, float c, floa
     return e4m3x4(coded(a, s), coded(b, s), coded(c, s), coded(d, s));
 }
 
-// The codes of a block's values, e4m3(v / s), from one reciprocal: y = RN(1 / s), the quotient v y and one correction by
-// its remainder, RN(q + (v - q s) y).  Before that last rounding it is within 2^-46 of v / s, relative, so that it is the
-// IEEE quotient unless v / s lies 2^-22 of an ulp or less from the middle of two FP32 numbers.  That matters for the code
-// only beside a rounding border of e4m3, a number of four significant bits; with significands V, S < 2^24 the middle beside
-// it, B 2^20 + 1 with B below 2^5, can be as near to V / S only where S is within 4 of a multiple of 2^20.  For those S
-// (16 either way) every V was checked on the CPU: always the IEEE quotient.  A code that is not 0 needs v >= s 2^-11, and
-// the remainder is a multiple of v 2^-47, which must not underflow; blocks outside that range, of zeros, with NaN or
-// infinities are divided.  (Bounding the quotient from both sides by two products costs less, but BF16 values lie on a
-// border too often: one in 200.)  All of it is done for -v / s, whose codes have the other sign: there the
-// correction adds zeros of one sign, while for v / s it made +0 of the code of -0.  Quantising 32768 x 2048 BF16 values took 106 us with a division each, and takes 39 us.
+// The codes of a block's values, e4m3(v / s), from one reciprocal: y = RN(1 / s), the quotient v y and one correction
+// by its remainder, RN(q + (v - q s) y).  Before that last rounding it is within 2^-46 of v / s, relative, so that it
+// is the IEEE quotient unless v / s lies 2^-22 of an ulp or less from the middle of two FP32 numbers.  That matters
+// for the code only beside a rounding border of e4m3, a number of four significant bits; with significands V, S <
+// 2^24 the middle beside it, B 2^20 + 1 with B below 2^5, can be as near to V / S only where S is within 4 of a
+// multiple of 2^20.  For those S (16 either way) every V is checked on the CPU, as is for every S the V beside each
+// border (tests/test_fp8_quotients.py): always the IEEE quotient.  A code that is not 0 needs v >= s 2^-11, and the
+// remainder is a multiple of v 2^-47, which must not underflow; blocks outside that range, of zeros, with NaN or
+// infinities are divided.  (Bounding the quotient from both sides by two products costs less, but BF16 values lie on
+// a border too often: one in 200.)  All of it is done for -v / s, whose codes have the other sign: there the
+// correction adds zeros of one sign, while for v / s it made +0 of the code of -0.  Quantising 32768 x 2048 BF16
+// values took 106 us with a division each, and takes 39 us.
 struct Coder {
     float s, y;
     bool fast;
