@@ -39,7 +39,7 @@ struct Waits {
     __device__ __forceinline__ int missing(int who, unsigned cta) const { return stall == who && blockIdx.x == cta; }
 };
 
-inline int64_t blocks_of(int64_t n) { return (n + kBlk - 1) / kBlk; }
+constexpr int64_t blocks_of(int64_t n) { return (n + kBlk - 1) / kBlk; }
 
 // --- device helpers ---------------------------------------------------------
 

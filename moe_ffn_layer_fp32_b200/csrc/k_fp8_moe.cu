@@ -168,9 +168,9 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
 
 constexpr int kN = 8;                  // tokens of a cluster
 constexpr int kCols = 16;              // the tokens' side of an MMA, its smallest: the other half is not used
-constexpr int kThreads = 224;          // producer, MMA, four promotion warps, MMA
+constexpr int kThreads = 224;          // producer, MMA, four promotion warps, MMA: each MMA warp has every second slot and buffer
 constexpr int kSlot = kBlk * kBlk;     // a ring slot: 16 KB
-constexpr int kMinRing = 2, kMaxRing = 12;
+constexpr int kMaxRing = 12;           // at least 4, and even (below)
 constexpr int kBufs = 8;               // TMEM buffers of 16 columns
 constexpr int kTmemCols = kBufs * kCols;
 constexpr int kUnit = 16;              // hidden features of a lane quarter
@@ -181,7 +181,6 @@ constexpr int kAlone = 16;             // (token, block) items that each CTA qua
 // of the hidden features.
 struct Layout {
     int ring;              // slots
-    int issuers;           // MMA warps: two, each with its own slots and buffers, or one for an odd ring
     int nu[2], no;         // units of 16 features (routed, shared) and of 32 output rows in a tile
     int operand;           // byte offsets
     int hidden, hidden_ld;
@@ -476,7 +475,7 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
         for (int j = max(i - lay.ring, 0); j < i; ++j) wait_drain(&sm->full[j % lay.ring], (j / lay.ring) & 1);
     } else if (warp == 1 || warp == 6) {
         int last = -1;
-        for (int i = warp == 1 ? 0 : lay.issuers == 2 ? 1 : steps; i < steps; i += lay.issuers) {
+        for (int i = warp == 1 ? 0 : 1; i < steps; i += 2) {
             const int s = i % lay.ring, b = i % kBufs;
             if ((i < 2 && gt > 0 && !warp_wait(&sm->xready, 0, &sm->stop, p.waits.err, 22)) ||
                 ((i == ngu || i == ngu + 1) && !warp_wait(&sm->hready, 0, &sm->stop, p.waits.err, 23)) ||
@@ -701,14 +700,14 @@ moe_experts_kernel(const __grid_constant__ CUtensorMap gu_map, const __grid_cons
     if (warp == 1) tc5::tmem_dealloc(tmem, kTmemCols);
 }
 
-// Ring slots and offsets for a cluster of S; at least two CTAs an SM where that leaves four slots each.
 // Of `all` units, dealt to S ranks: how many a tile takes (4 at most, none more than a rank needs).
-int tile_units(int all, int S) {
+constexpr int tile_units(int all, int S) {
     const int most = (all + S - 1) / S, tiles = (most + 3) / 4;
     return (most + tiles - 1) / tiles;
 }
 
-Layout layout_for(const MoePlan& p, int S) {
+// Ring slots and offsets for a cluster of S.
+constexpr Layout layout_for(const MoePlan& p, int S) {
     const int ph = std::min(p.part_hidden, p.hs), hm = std::max(p.h, ph), KBd = (int)blocks_of(p.d), KBh = (int)blocks_of(hm);
     Layout l = {};
     l.nu[0] = tile_units(p.h / kUnit, S);
@@ -720,9 +719,7 @@ Layout layout_for(const MoePlan& p, int S) {
     // two CTAs an SM where that leaves four slots each; less static shared memory and alignment
     const int half = 113 * 1024 - 4096, whole = 226 * 1024 - 4096;
     const int room = (half - rest) / kSlot >= 4 ? half : whole;
-    l.ring = std::min((room - rest) / kSlot, kMaxRing);
-    if (l.ring > 3) l.ring &= ~1;
-    l.issuers = l.ring % 2 ? 1 : 2;
+    l.ring = std::min((room - rest) / kSlot, kMaxRing) & ~1;
     l.operand = l.ring * kSlot;
     l.hidden = l.operand + operand;
     l.sx = l.hidden + hidden;
@@ -730,6 +727,15 @@ Layout layout_for(const MoePlan& p, int S) {
     l.bytes = l.sh + KBh * kN * 4;
     return l;
 }
+
+// The largest layer that the entry takes leaves six slots; a smaller one takes less beside the ring.
+constexpr MoePlan largest_plan() {
+    MoePlan p = {};
+    p.d = 8192;
+    p.h = p.hs = p.part_hidden = 4096;
+    return p;
+}
+static_assert(layout_for(largest_plan(), 4).ring == 6 && layout_for(largest_plan(), 8).ring >= 6, "ring slots");
 
 // Gate and up rows: (k, row of a unit, gate or up, unit, expert), so that one copy brings a tile as the kernel wants it.
 cudaError_t gate_up_map(CUtensorMap* m, const uint8_t* w, int d, int H, int E, int nu) {
@@ -750,7 +756,6 @@ template <int S>
 cudaError_t launch_experts(const MoePlan& p, int clusters, cudaStream_t st) {
     static_assert(S <= kRanks, "one counter a rank");
     const Layout l = layout_for(p, S);
-    if (l.ring < kMinRing) return cudaErrorInvalidValue;
     CUtensorMap m[4];
     cudaError_t e = gate_up_map(&m[0], p.gate_up, p.d, p.h, p.E, l.nu[0]);
     if (e == cudaSuccess) e = down_map(&m[1], p.down, p.d, p.h, p.E, l.no);
@@ -820,7 +825,7 @@ cudaError_t launch_moe_few(const MoePlan& p, cudaStream_t st) {
     // (64 tokens of 2048 features: 104 us with 8, 81 us with 4).
     const int slots = p.T * p.k;
     const int busy = (p.T + kN - 1) / kN * p.parts + std::min(p.E, slots), clusters = busy + slots / kN;
-    if (8 * busy <= 2 * sm_count() || layout_for(p, 4).ring < 4) return launch_experts<8>(p, clusters, st);
+    if (8 * busy <= 2 * sm_count()) return launch_experts<8>(p, clusters, st);
     return launch_experts<4>(p, clusters, st);
 }
 
