@@ -280,7 +280,7 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                 const int nt = (int)(L - mt * ntiles);
                 int g = 0;
                 int64_t row0 = mt * kRows, rows = p.M;
-                if (p.groups ? !groups.find(p, lane, mt, g, row0, rows) : L >= total) {
+                if (!kPair && p.groups ? !groups.find(p, lane, mt, g, row0, rows) : L >= total) {  // (groups go to single CTAs)
                     if (lane == 0) {
                         ti.end = 1;
                         mbar_arrive(&sm->tfull[b]);
