@@ -400,7 +400,9 @@ mmoe_status mmoe_forward_static_scratch(const mmoe_config* cfg, const mmoe_weigh
  *
  * These calls keep no state: they run on the current device, which must own
  * every buffer, on any stream, also in a stream capture, and calls on buffers
- * of their own may overlap on the GPU.  Outputs must not overlap inputs.
+ * of their own may overlap on the GPU.  Outputs must not overlap inputs; a
+ * buffer counts as all of its bytes from the first row's first to the last
+ * row's last, so that rows of two tensors may not alternate in memory either.
  * Errors of all of them: INVALID_ARG (a NULL pointer, a size, stride, type or
  * alignment out of range, overlapping buffers), CUDA, and from the products and
  * the layer TIMEOUT: a bounded wait of an earlier product or layer call on this
@@ -420,8 +422,10 @@ mmoe_status mmoe_quantize_fp8_blocks(const void* w, int32_t w_type, int64_t batc
                                      float* s, void* stream);
 
 /* y[M, N] = a[M, K] w[N, K]^T from codes and scales: per block of K the FP32
- * sum of the products of codes, times both scales, added in FP32 over the
- * blocks and rounded once to y's type (row stride ldy elements).  M = 0 is a
+ * sum of the products of codes, times the FP32 product of both scales, added in
+ * FP32 over the blocks and rounded once to y's type (row stride ldy elements).
+ * Where the product of two scales overflows, its block gives infinities and,
+ * where its sum is 0, NaN; where it is subnormal, it has fewer bits.  M = 0 is a
  * no-op.  K a multiple of 16; N any; a and w 16-byte aligned. */
 mmoe_status mmoe_gemm_fp8(const uint8_t* a, const float* sa, int64_t M, const uint8_t* w, const float* sw, int64_t N,
                           int64_t K, void* y, int32_t y_type, int64_t ldy, void* stream);
@@ -448,7 +452,9 @@ mmoe_status mmoe_linear_fp8(const uint16_t* x_bf16, int64_t M, int64_t ldx, cons
 
 /* The MoE layer, Eq. (*), on such weights: FFN(x) = down(Q(silu(gate Q(x)) *
  * (up Q(x)))), Q the quantisation of a row as above, silu and the products in
- * FP32, the router (FP32 weights) on x itself; the expert rows are added in
+ * FP32, the router on x itself (FP32 weights and FP32 sums: experts whose keys
+ * differ by less than those sums' rounding may be ranked either way, equal FP32
+ * keys go to the lower index); the expert rows are added in
  * the order of Eq. (*), y = FFN_s + g_0 FFN_0 + ..., so that y is
  * bit-reproducible (a token's y does not depend on its batch either).  An
  * FFN_s wider than an expert is summed in parts of ceil(h / 128) * 128 hidden
@@ -474,7 +480,7 @@ typedef struct {
 } mmoe_fp8_weights;
 
 /* y [T, d] (y_type) from x (BF16 [T, d], 16-byte aligned), for T up to
- * min(64, max_tokens): two launches.  Optional outputs as in mmoe_forward.
+ * min(64, max_tokens): two launches.  There is no form for more tokens.  Optional outputs as in mmoe_forward.
  * The workspace (device, 256-byte aligned, the size that mmoe_fp8_workspace
  * writes to *bytes) needs no clearing and holds nothing between calls; calls
  * that may overlap on the GPU, replays of two captured graphs among them, need

@@ -11,20 +11,24 @@
 // rows x H x 128 columns.  The rows are the MMA's M: each thread of the promotion warps owns one row, so a scale is one
 // register a block, and its columns stay in registers.  Warps:
 //   0      producer: per block of 128 the activation and the weight tile (TMA, 128-byte swizzle)
-//   1, 2   issue the MMAs, a block in turn, into 512 / (128 H) buffers of TMEM
-//   3      idle (it completes warpgroup 0, whose registers go to the promotion)
+//   1, 2   issue the MMAs, a block in turn, into 512 / (128 H) buffers of TMEM (tiles of 128 x 256: warp 1 alone)
+//   3      idle (it completes warpgroup 0, whose registers go to the promotion; so is warp 2 there)
 //   4..11  promotion and epilogue: warp w reads TMEM lanes 32 (w % 4).. and half of the columns; y goes out through
 //          shared memory by the copy engine, while the next tile is on its way
-// What bounds it: the handoffs.  For 16384 x 2048 x 2048 (75 us; 1.83 PFLOP/s) a block takes about 800 clocks, of which the
-// MMAs run 515; without the additions it takes 725, without the TMEM loads 550, without the copies no less.  More buffers
-// of half the width, four promotion warps a half, FFMA2, a poll of the next buffer ahead of time and 16-byte stores by the
-// warps themselves were all slower or no faster.
+// What bounds it: the handoffs, and the ends of tiles.  16384 x 2048 x 2048 takes 70 us (1.96 PFLOP/s) at 1.67 GHz, 117,800
+// clocks a CTA, by clocks read in the promotion warps: seven tiles of 16 blocks at 750 clocks (of which a block's MMAs run
+// 515) and 2,150 to stage and store y, while the MMAs run only as far ahead as there are buffers, then 300 to the next
+// tile's first block; 3,700 before the first tile and 3,000 after the last; the rest is the wait for the launch before.
+// Without the additions a block took 725 of then 800 clocks, without the TMEM loads 550, without the copies no less.  More
+// buffers of half the width, four promotion warps a half, FFMA2, a poll of the next buffer ahead of time and 16-byte stores
+// by the warps themselves were all slower or no faster.
 //
 // product_small_kernel (up to 64 rows).  Bound by one pass over the weights and its own latencies, so these are the MMA's M
 // (128 weight rows) and the few activation rows its N; a cluster splits the blocks of 128 along K so that every SM streams,
 // and adds its partial sums through distributed shared memory in a fixed order.  1 x 2048 x 1024: 3.6 us a launch in a
-// chain (with 200 KB of shared memory instead of half, which keeps the next launch off the SM, 7.5 us); 64 x 4096 x 2048: 11.0
-// us, half of it for the codes of the rows, which every cluster makes for itself.
+// chain (with 200 KB of shared memory instead of half, which keeps the next launch off the SM, 7.5 us), 3.8 us where each
+// launch's weights come from HBM; 64 x 4096 x 2048: 11.0 and 11.3 us, half of it for the codes of the rows, which every
+// cluster makes for itself.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -851,10 +855,14 @@ cudaError_t launch_product(const Product& p, cudaStream_t st) {
     const int64_t nb = blocks_of(p.N), wide = (nb + 1) / 2, pairs = row_tiles(2 * kBlk) * wide, singles = row_tiles(kBlk) * wide;
     e = byte_map(&wm, p.w, (uint64_t)p.K, (uint64_t)(G * p.N), (uint64_t)p.K, kBlk);
     if (e != cudaSuccess) return e;
-    // Dense rows go to pairs of CTAs where there are tiles for all of them (32768 x 2048 x 2048 with its quantisation: 221 us,
-    // 232 us with tiles of 128 x 256).  Groups fill 256 rows less often (8192 rows in 60 groups: 24 us with tiles of 128 x 256, 30 us with
-    // pairs; 32768 rows: 127 us and 130 us).  Where there are too few of either, tiles of 128 x 128 (777 x 1000 x 784: 9.5
-    // us, 12 us with the others).
+    // Dense rows go to pairs of CTAs where there are tiles for all of them (32768 x 2048 x 2048 with its quantisation: 175
+    // us, 186 us with tiles of 128 x 256, 207 us with 128 x 128).  Groups fill 256 rows less often, and go to tiles of 128 x
+    // 256 (8192 rows in 60 groups, 1024 x 1024: 23.7 us, 25.8 us with 128 x 128, and 30 us with pairs when those still
+    // walked over groups; 32768 rows, 1536 x 1536: 105 and 119 us).  The number of their tiles is known as an upper bound
+    // only, but from a few rows up the wide tiles are the better ones (256 rows: 17.1 and 18.9 us, 64 rows: 15.4 and 16.4 us,
+    // 16 rows the same).  Where there are too few of either, tiles of 128 x 128, more of them (777 x 1000 x 784: 9.4 us, 12.5
+    // us with 128 x 256 and 11.8 us with pairs; 512 x 2048 x 2048: 10.5 us and 14.2 us with either).  K does not enter, and
+    // no tile's K is split: between the two, at 1200 to 2048 x 2048 x 2048, the smaller tiles are up to 7 % behind.
     if (nb > 1 && !p.groups && p.M > kBlk && 2 * pairs >= sm_count()) return launch_many<2, 2>(p, am, wm, pairs, st);
     if (nb > 1 && singles >= sm_count()) return launch_many<1, 2>(p, am, wm, singles, st);
     return launch_many<1, 1>(p, am, wm, row_tiles(kBlk) * nb, st);

@@ -84,7 +84,9 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const T* x, int
     }
 }
 
-// Weights: one CTA per 128 x 128 block; a half warp takes a row at a time.
+// Weights: one CTA per 128 x 128 block; a half warp takes a row at a time.  60 x 2048 x 2048 FP32 values take 190 us, the
+// time of their traffic; BF16 ones take 379 us for 115 us of traffic, and have not been made faster (weights are quantised
+// once).
 template <class T>
 __global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(const T* w, int nb, int kb, int N,
                                                                    int K, uint8_t* q,

@@ -8,11 +8,16 @@
 // All of it in FP32: r' is rounded where it is stored, x' is computed from the
 // sum before that rounding, and the codes from x' before its rounding to BF16.
 //
-// Bound by memory: a row is read once, held in registers through both norms
+// Bound by memory: a row is read once, held by its threads through both norms
 // and written once.  kG threads take a row, 8 features each (16-byte accesses,
 // 16 lanes side by side on one block of 128 features), and go on to other rows:
 // the weights and a gate per feature are read once a thread, and the next row
-// is on its way while this one is reduced.
+// is on its way while this one is reduced.  Rows of 2048 features stay in
+// registers and run at 90 % of the memory's rate (32768 rows with codes: 126
+// us).  Above that a thread has 64 registers, 92 to 136 bytes of which spill,
+// and the barriers of 16 or 32 warps weigh more: 8192 rows of 4096 take 98 us
+// for 56 us of traffic, of 8192 237 us for 113.  (Rows of up to 256, a warp
+// each, spill up to 76 bytes where r is FP32.)
 #include <algorithm>
 
 #include "fp8.cuh"
@@ -55,7 +60,8 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
 // 1 / sqrt(mean(v^2) + eps) of the row that kG threads hold.  `part` holds one word a warp; the next row uses another
 // one, so that one barrier is enough.  Every thread does the last steps, so they are a product with 1 / d (inv_d) and
 // rsqrtf (off by 2 ulp at most): with IEEE divisions and root the kernel issued 430 instructions a warp and row, and
-// was bound by them.
+// was bound by them.  Of 32768 x 2048 codes 66 differ
+// from those of a 64-bit norm, 78 with torch's FP32 operations (IEEE root and quotient).
 template <int kG>
 __device__ __forceinline__ float inv_rms(const float (&v)[8], float* part, float inv_d, float eps) {
     float sum = 0.0f;

@@ -167,7 +167,8 @@ def _optional(t: torch.Tensor | None, shape: tuple, dtype, name: str):
 
 
 class FP8MoELayer:
-    """The MoE feed-forward layer (Eq. (*) of the MobileMoE pages) on e4m3 weights, for up to 64 tokens a call.
+    """The MoE feed-forward layer (Eq. (*) of the MobileMoE pages) on e4m3 weights, for up to 64 tokens a call (more are
+    refused: a prompt takes calls of 64, each of which reads the selected experts' weights again).
 
     ``load`` keeps the caller's tensors and reads them in place; every ``forward`` allocates its own workspace, so that
     calls on several streams, and captured graphs, do not share one."""
