@@ -37,7 +37,7 @@ def _output(y, M: int, N: int, out_dtype, x: torch.Tensor):
         if out_dtype not in TYPE:
             raise ValueError("out_dtype must be float32 or bfloat16")
         return empty(x, M, N, out_dtype), TYPE[out_dtype], N
-    if y.dtype not in TYPE or y.shape[0] != M:
+    if y.dtype not in TYPE or y.dim() != 2 or y.shape[0] != M:
         raise ValueError(f"y must be a float32 or bfloat16 tensor of {M} rows")
     return y, TYPE[y.dtype], rows_of(y, N, "y")
 

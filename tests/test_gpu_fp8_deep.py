@@ -1,8 +1,10 @@
-"""Products of many blocks of K in the larger tiles against 64-bit sums (on the GPU, of the values that the codes stand for)."""
+"""Products of many blocks of K in the larger tiles against 64-bit sums (on the GPU, of the values that the codes stand for);
+refusals of outputs of other shapes; the layer's clusters of 4 against those of 8."""
 import pytest
 import torch
 
 from tests import fp8_util as U
+from tests import test_gpu_fp8_moe as moe
 from tests.test_gpu_fp8 import fp8, gen  # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +44,25 @@ def test_deep_groups(fp8, dtype):  # noqa: F811
     for g, (_, _, w) in enumerate(parts):
         rows = slice(int(off[g]), int(off[g + 1]))
         U.assert_within(y[rows], (a[rows] @ w.t()).cpu(), U.product_bound(a[rows], w, k).cpu(), dtype)
+
+
+def test_outputs_of_other_shapes_are_refused(fp8):  # noqa: F811
+    xq, xs, _ = operand(5, 144, 5, 20)
+    wq, ws, _ = operand(40, 144, 1, 22)
+    off = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    x = torch.zeros(5, 144, dtype=BF16, device="cuda")
+    for y in (torch.empty((), device="cuda"), torch.empty(5, device="cuda"), torch.empty(5, 40, 1, device="cuda"),
+              torch.empty(40, 5, device="cuda").t(), torch.empty(1, 40, device="cuda").expand(5, 40)):
+        for call in (lambda: fp8.gemm_fp8(xq, xs, wq, ws, y), lambda: fp8.linear_fp8(x, wq, ws, y),
+                     lambda: fp8.grouped_gemm_fp8(xq, xs, off, wq[None], ws[None], y)):
+            with pytest.raises(ValueError):
+                call()
+
+
+def test_layer_in_clusters_of_four_and_of_eight(fp8):  # noqa: F811
+    """64 tokens on 60 experts run in clusters of 4 CTAs, a few of them in clusters of 8: the same bits."""
+    c = moe.Case(512, 288, 416, 60, 4, seed=30)
+    layer, x = c.layer(fp8), c.x(64).cuda()
+    whole = layer.forward(x)
+    for a, b in ((0, 1), (3, 11), (50, 64)):
+        assert torch.equal(layer.forward(x[a:b]), whole[a:b])
