@@ -329,15 +329,9 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                     __syncwarp();
                 }
             }
-            // Every copy has landed before the CTA may exit.  CTA 0's barriers count those of both; after a wait that gave up
-            // CTA 1 may have sent others, which no barrier tells of: they are given about 1 ms.
-            if (rank == 0) {
+            // every copy has landed before the CTA may exit; CTA 0's barriers count those of both
+            if (rank == 0)
                 for (int i = max(sc - S, 0); i < sc; ++i) wait_drain(&sm->full[i % S], (i / S) & 1);
-            } else if (sm->stop.is_set()) {
-                const long long t0 = async::clk();
-                while (async::clk() - t0 < kLandClk) {
-                }
-            }
         } else if (warp <= kIssuers) {
             // Two warps issue in turn, a block of K each: its MMAs run for 515 clocks (a pair) or 288, but what one warp
             // does for it (two waits, four MMAs, two commits) takes about 600.  (The MMAs of a single CTA's wide tile wait
@@ -503,6 +497,13 @@ product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
     tc5::before_sync();
     __syncthreads();
     if (kPair) {  // neither CTA leaves while the other may signal its barriers or the pair's MMAs read its operands
+        // after a wait that gave up CTA 1 may have sent copies that CTA 0 did not, which no barrier tells of: they get about 1 ms
+        if (rank != 0 && sm->stop.is_set()) {
+            const long long t0 = async::clk();
+            while (async::clk() - t0 < kLandClk) {
+            }
+            __syncwarp();
+        }
         cluster_arrive();
         cluster_wait();
     }
